@@ -588,6 +588,101 @@ int trace_replay_direction(const uint8_t* bits, const uint8_t* scales, int scale
                            const uint16_t* resid, uint16_t* x_hat, uint8_t* codes_out,
                            unsigned long long* corrections, quads_stream_t stream);
 
+/* ---------------------------------------- NVFP4 key/value cache, attention
+ * [TRACE] "Le problème", "Résultats": the rollout keeps weights, activations
+ * and the KV cache in FP4.  The pages give no layout, no scale rule and no
+ * attention; the readings here are the plainest that serve them: a paged
+ * cache on the grid of every other NVFP4 tensor of this library, softmax
+ * attention with grouped query heads, and rotary positions.
+ *
+ * A cache holds n_pages pages of page_size tokens for n_heads key/value
+ * heads of head_dim elements, keys and values alike:
+ *   codes  [n_pages][n_heads][page_size][head_dim / 2], packed E2M1;
+ *   scales [n_pages][n_heads][page_size][head_dim / 16], E4M3, one per 16
+ *          consecutive elements of a head (the sign bit is not read);
+ *   g      device float[n_heads]: the decode scale of each head, given by the
+ *          caller (calibrated: max |k| of the head / 2688) and fixed while
+ *          tokens written with it are in use.
+ * value = e2m1 * e4m3 * g.  head_dim is 64 or 128, page_size a multiple of
+ * 16 up to 65536, n_heads at most 1024, n_pages < 2^31; the four arrays
+ * 16-byte aligned.
+ *
+ * Sequences (all device int32): row_off [n_seqs + 1], ascending from 0: rows
+ * row_off[b] .. row_off[b + 1] - 1 of a call belong to sequence b, rows behind
+ * the last belong to none.  kv_len [n_seqs]: the tokens of each sequence in
+ * the cache, this call's rows among them, as its last: row i of sequence b
+ * has position kv_len[b] - (row_off[b + 1] - row_off[b]) + i.  block_table
+ * [n_seqs][max_pages]: the page of positions j * page_size ...; an entry
+ * outside [0, n_pages), and any position past max_pages * page_size, has no
+ * page.  n_seqs <= 65535. */
+typedef struct quads_kv_cache {
+  int64_t n_pages;
+  int32_t page_size, n_heads, head_dim, reserved;
+  uint8_t* k_codes;
+  uint8_t* k_scales;
+  uint8_t* v_codes;
+  uint8_t* v_scales;
+  const float* g_k;
+  const float* g_v;
+} quads_kv_cache;
+
+/* Quantizes the new tokens' keys and values into their pages, with the
+ * operations of quads_quantize_nvfp4 and the given decode scales (blocks
+ * above a head's calibrated range saturate).  k, v: BF16 [rows][n_heads][D],
+ * rows ld_k and ld_v elements apart (multiples of 8), 16-byte aligned, finite.
+ * Rows without a page or with a negative position are dropped.  Two rows of
+ * one call that name the same place of a page leave it undefined (each block
+ * may come from either). */
+int quads_kv_cache_write(const quads_kv_cache* cache, const uint16_t* k, const uint16_t* v, int64_t rows,
+                         int64_t ld_k, int64_t ld_v, const int32_t* row_off, const int32_t* kv_len,
+                         const int32_t* block_table, int n_seqs, int max_pages, quads_stream_t stream);
+/* Reads tokens back ([TRACE] "Fonctionnement": the trainer reproduces the
+ * rollout's values): row row_off[b] + i of k_out and v_out [rows][n_heads][D]
+ * is position start[b] + i of sequence b (start NULL: 0), e2m1 * e4m3 * g as
+ * FP32 or rounded to BF16 (out_dtype), zeros where there is no page.  Rows of
+ * no sequence are untouched.  Either output may be NULL. */
+int quads_kv_cache_read(const quads_kv_cache* cache, const int32_t* row_off, const int32_t* start,
+                        const int32_t* block_table, int n_seqs, int max_pages, int64_t rows, void* k_out,
+                        void* v_out, int out_dtype, quads_stream_t stream);
+/* Rotary positions of queries and keys (NULL and 0 heads: without that one).
+ * BF16 rows of heads_q (heads_k) heads of head_dim elements, ld elements
+ * apart (multiples of 8), 16-byte aligned; the outputs may be the inputs.
+ * The first rot_dim elements of a head turn in pairs f = 0 .. rot_dim / 2 - 1
+ * of elements (f, f + rot_dim / 2), or (2f, 2f + 1) when interleaved:
+ *   a' = m (a cos t - b sin t), b' = m (b cos t + a sin t),
+ *   t = positions[row] * freq[f] (in 64 bits), m = mscale;
+ * the others are copied.  inverse = 1 turns by -t: the gradient with respect
+ * to the input from the one with respect to the output.  positions: device
+ * int64[T]; freq: device double[rot_dim / 2], radians per position.
+ * rot_dim and head_dim: multiples of 16, rot_dim <= head_dim <= 1024. */
+int quads_rope(const uint16_t* q, int64_t ld_q, int heads_q, const uint16_t* k, int64_t ld_k, int heads_k,
+               int64_t T, int head_dim, const int64_t* positions, const double* freq, int rot_dim,
+               int interleaved, float mscale, int inverse, uint16_t* q_out, int64_t ld_q_out,
+               uint16_t* k_out, int64_t ld_k_out, quads_stream_t stream);
+/* Attention of the new tokens over the cache:
+ *   out[r][h] = bf16(sum_j softmax_j(scale q[r][h] . k_j) v_j)
+ * over the positions j of r's sequence that have a page, j <= p (r's own
+ * position) and, when window > 0, j > p - window; k and v are the cached
+ * values of head h / (heads_q / n_heads).  A row with no such j gets zeros.
+ *   q, out    BF16 [rows][heads_q][D], q's rows ld_q elements apart
+ *             (a multiple of 8), out's contiguous; 16-byte aligned.  heads_q
+ *             is a multiple of n_heads.  out must not overlap q.
+ *   max_q_len at least the rows of the longest sequence (a longer sequence's
+ *             rows past it are not computed); the work is laid out by it.
+ *   lse       (nullable) device float [rows][heads_q]: log sum_j exp(scale
+ *             q . k_j), -inf for a row of zeros.
+ *   ws        device workspace of quads_attention_paged_workspace_bytes()
+ *             bytes, 16-byte aligned; calls that can run at the same time
+ *             need their own.
+ * Scores, softmax statistics and sums are FP32.  A device wait that exceeds
+ * ~4 s records a timeout (quads_device_status). */
+size_t quads_attention_paged_workspace_bytes(const quads_kv_cache* cache, int64_t rows, int heads_q, int n_seqs,
+                                             int max_pages, int max_q_len);
+int quads_attention_paged(const uint16_t* q, int64_t rows, int64_t ld_q, int heads_q, const quads_kv_cache* cache,
+                          const int32_t* row_off, const int32_t* kv_len, const int32_t* block_table, int n_seqs,
+                          int max_pages, int max_q_len, float scale, int window, uint16_t* out, float* lse,
+                          void* ws, size_t ws_bytes, quads_stream_t stream);
+
 /* ------------------------------------------------------ layer stacking
  * The pages describe the MoE layer, not the model around it; a stack of
  * layers is joined here in the plainest way: x_{l+1} = x_l + MoE_l(x_l), and

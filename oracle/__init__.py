@@ -33,6 +33,7 @@ Modules:
   trace    -- rollout record export and trainer replay
   layer    -- one MoE layer on both sides, composed from the steps above
   stack    -- router projection and residual connection between layers
+  kvcache  -- the paged NVFP4 key/value cache, attention over it, rotary positions
 
 Pins: every function here is checked in ``tests/test_oracle_*.py`` against
 brute force, closed forms, library routines or invariants.  Functions with

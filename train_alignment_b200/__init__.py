@@ -5,4 +5,4 @@ ABI declared in ``include/quads.h``); ``binding`` marshals torch tensors to
 it.  Importing this package does not load the library; the first call does,
 and raises if it is missing.
 """
-__all__ = ["binding", "workloads"]
+__all__ = ["attention", "binding", "workloads"]

@@ -1,0 +1,85 @@
+"""The rollout's key/value cache in NVFP4, and the frequencies of rotary positions.
+
+[TRACE] "Le problème", "Résultats": the rollout keeps weights, activations
+and the KV cache in FP4.  KVCache holds the pages and their decode scales; it
+is written with binding.kv_cache_write, attended with
+binding.attention_paged and read back with binding.kv_cache_read.
+"""
+import ctypes
+import math
+
+import torch
+
+from . import binding as B
+
+
+class KVCache:
+    """A paged NVFP4 key/value cache: codes [n_pages, n_heads, page_size, D / 2],
+    scales [n_pages, n_heads, page_size, D / 16], decode scales g [n_heads].
+    Wraps the given tensors; KVCache.empty allocates them."""
+
+    def __init__(self, k_codes, k_scales, v_codes, v_scales, g_k, g_v):
+        n_pages, n_heads, page_size, half = k_codes.shape
+        self.n_pages, self.n_heads, self.page_size, self.head_dim = n_pages, n_heads, page_size, 2 * half
+        scales = (n_pages, n_heads, page_size, half // 8)
+        for t, dt, shape, name in ((k_codes, torch.uint8, (n_pages, n_heads, page_size, half), "k_codes"),
+                                   (v_codes, torch.uint8, (n_pages, n_heads, page_size, half), "v_codes"),
+                                   (k_scales, torch.uint8, scales, "k_scales"),
+                                   (v_scales, torch.uint8, scales, "v_scales"),
+                                   (g_k, torch.float32, (n_heads,), "g_k"), (g_v, torch.float32, (n_heads,), "g_v")):
+            if t.dtype != dt or tuple(t.shape) != shape or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous {dt} tensor of shape {shape}, got {t.dtype} "
+                                 f"{tuple(t.shape)}")
+            if t.device != k_codes.device:
+                raise ValueError(f"{name} is on {t.device}, k_codes on {k_codes.device}")
+        self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
+        self.g_k, self.g_v = g_k, g_v
+        self.desc = B.KVCacheDesc(n_pages, page_size, n_heads, 2 * half, 0, k_codes.data_ptr(), k_scales.data_ptr(),
+                                  v_codes.data_ptr(), v_scales.data_ptr(), g_k.data_ptr(), g_v.data_ptr())
+        self.ref = ctypes.byref(self.desc)
+
+    @classmethod
+    def empty(cls, n_pages, page_size, n_heads, head_dim, amax_k, amax_v, device="cuda"):
+        """Pages of zeros for heads whose largest |k| and |v| are amax_k and
+        amax_v (tensors [n_heads], or one number for all heads)."""
+        def g(a):
+            a = torch.as_tensor(a, dtype=torch.float32, device=device).expand(n_heads)
+            return (a / 2688.0).contiguous()
+        z = lambda d: torch.zeros((n_pages, n_heads, page_size, d), dtype=torch.uint8, device=device)
+        return cls(z(head_dim // 2), z(head_dim // 16), z(head_dim // 2), z(head_dim // 16), g(amax_k), g(amax_v))
+
+
+def rope_frequencies(rot_dim, theta=10000.0, scaling=None, factor=1.0, original_len=None, low=1.0, high=32.0,
+                     device="cuda"):
+    """Radians per position of each of the rot_dim / 2 pairs, float64, for
+    binding.rope: theta ** (-2 f / rot_dim), changed for contexts `factor`
+    times as long as `original_len`:
+      scaling None       unchanged;
+      "linear"           divided by factor (positions interpolated);
+      "base"             theta * factor ** (rot_dim / (rot_dim - 2)), so that the
+                         slowest pair is divided by factor and the fastest kept;
+      "by_turns"         pairs that turn at most `low` times in original_len
+                         positions divided by factor, those that turn at least
+                         `high` times kept, those between mixed linearly in
+                         their turns.
+    """
+    if rot_dim < 2 or rot_dim % 2:
+        raise ValueError("rot_dim must be a positive even number")
+    if not factor > 0:
+        raise ValueError("factor must be positive")
+    f = torch.arange(rot_dim // 2, dtype=torch.float64)
+    if scaling == "base":
+        if rot_dim < 4:
+            raise ValueError('scaling "base" needs rot_dim >= 4')
+        theta = theta * factor ** (rot_dim / (rot_dim - 2))
+    freq = float(theta) ** (-2.0 * f / rot_dim)
+    if scaling == "linear":
+        freq = freq / factor
+    elif scaling == "by_turns":
+        if original_len is None or not high > low:
+            raise ValueError('scaling "by_turns" needs original_len and low < high')
+        keep = ((freq * original_len / (2.0 * math.pi) - low) / (high - low)).clamp(0.0, 1.0)
+        freq = freq * (keep + (1.0 - keep) / factor)
+    elif scaling not in (None, "base"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    return freq.to(device)

@@ -55,6 +55,12 @@ class TraceQTensorSrc(ctypes.Structure):
                 ("resid", c_vp)]
 
 
+class KVCacheDesc(ctypes.Structure):
+    _fields_ = [("n_pages", c_i64), ("page_size", ctypes.c_int32), ("n_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("reserved", ctypes.c_int32), ("k_codes", c_vp), ("k_scales", c_vp),
+                ("v_codes", c_vp), ("v_scales", c_vp), ("g_k", c_vp), ("g_v", c_vp)]
+
+
 _SIGS = {
     "quads_last_error": (ctypes.c_char_p, []),
     "quads_abi_version": (c_i32, []),
@@ -108,6 +114,13 @@ _SIGS = {
     "quads_fakequant_weight_ste_gate_up": (c_i32, [c_vp, c_i64, c_i64, c_i64, c_vp, c_i32, c_vp, c_vp, c_vp, c_vp,
                                                    c_vp, c_i32, c_i32, c_vp, c_vp, c_sz, c_vp]),
     "quads_fakequant_weight_ste_backward": (c_i32, [c_vp, c_vp, c_i64, c_i32, c_vp]),
+    "quads_kv_cache_write": (c_i32, [c_vp, c_vp, c_vp, c_i64, c_i64, c_i64, c_vp, c_vp, c_vp, c_i32, c_i32, c_vp]),
+    "quads_kv_cache_read": (c_i32, [c_vp, c_vp, c_vp, c_vp, c_i32, c_i32, c_i64, c_vp, c_vp, c_i32, c_vp]),
+    "quads_rope": (c_i32, [c_vp, c_i64, c_i32, c_vp, c_i64, c_i32, c_i64, c_i32, c_vp, c_vp, c_i32, c_i32,
+                           ctypes.c_float, c_i32, c_vp, c_i64, c_vp, c_i64, c_vp]),
+    "quads_attention_paged_workspace_bytes": (c_sz, [c_vp, c_i64, c_i32, c_i32, c_i32, c_i32]),
+    "quads_attention_paged": (c_i32, [c_vp, c_i64, c_i64, c_i32, c_vp, c_vp, c_vp, c_vp, c_i32, c_i32, c_i32,
+                                      ctypes.c_float, c_i32, c_vp, c_vp, c_vp, c_sz, c_vp]),
     "quads_router_logits": (c_i32, [c_vp, c_i64, c_i64, c_vp, c_i32, c_vp, c_vp]),
     "quads_residual_add": (c_i32, [c_vp, c_vp, c_i64, c_vp, c_vp]),
     "trace_qrecord_layout": (c_sz, [c_i32, c_i64, c_i32, c_vp, c_i32, c_vp]),
@@ -673,4 +686,145 @@ def residual_add(x, y, out=None):
     _dev(y, torch.bfloat16, "y")
     out = out if out is not None else torch.empty_like(x)
     _check(load().quads_residual_add(_p(x), _p(y), x.numel(), _p(out), _s()), "quads_residual_add")
+    return out
+
+
+# ------------------------------------------------ KV cache, rope, attention
+
+
+def _here(t, name):
+    """A CUDA tensor of the current device (the one the call's stream and
+    launches belong to)."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, not on the current device cuda:{torch.cuda.current_device()}")
+
+
+def _ints(t, dtype, shape, name):
+    _here(t, name)
+    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape}, got {t.dtype} {tuple(t.shape)}")
+
+
+def _heads_view(x, name):
+    """A BF16 tensor [rows, heads, dim] whose rows may be strided: (rows, heads, dim, row stride)."""
+    _here(x, name)
+    if x.dtype != torch.bfloat16 or x.dim() != 3:
+        raise ValueError(f"{name} must be a bfloat16 tensor [rows, heads, dim]")
+    rows, heads, dim = x.shape
+    if (x.stride(2) != 1 and dim > 1) or (x.stride(1) != dim and heads > 1):
+        raise ValueError(f"{name}: the heads of a row must be contiguous")
+    ld = x.stride(0) if rows > 1 else heads * dim
+    return rows, heads, dim, ld
+
+
+def _tables(cache, row_off, block_table):
+    """Checks the cache's device, row_off and block_table; (n_seqs, max_pages)."""
+    _here(cache.k_codes, "the cache")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [n_seqs, max_pages]")
+    n_seqs, max_pages = block_table.shape
+    _ints(block_table, torch.int32, (n_seqs, max_pages), "block_table")
+    _ints(row_off, torch.int32, (n_seqs + 1,), "row_off")
+    return n_seqs, max_pages
+
+
+def kv_cache_write(cache, k, v, row_off, kv_len, block_table):
+    """Quantize k, v [rows, n_heads, D] into the cache's pages (quads_kv_cache_write)."""
+    rows, heads, dim, ld_k = _heads_view(k, "k")
+    rows_v, heads_v, dim_v, ld_v = _heads_view(v, "v")
+    if (heads, dim) != (cache.n_heads, cache.head_dim) or (rows_v, heads_v, dim_v) != (rows, heads, dim):
+        raise ValueError(f"k and v must be [rows, {cache.n_heads}, {cache.head_dim}], got {tuple(k.shape)} and "
+                         f"{tuple(v.shape)}")
+    n_seqs, max_pages = _tables(cache, row_off, block_table)
+    _ints(kv_len, torch.int32, (n_seqs,), "kv_len")
+    _check(load().quads_kv_cache_write(cache.ref, _p(k), _p(v), rows, ld_k, ld_v, _p(row_off), _p(kv_len),
+                                       _p(block_table), n_seqs, max_pages, _s()), "quads_kv_cache_write")
+
+
+def kv_cache_read(cache, row_off, block_table, rows, start=None, out_dtype=OUT_BF16, k_out=None, v_out=None):
+    """Cached keys and values [rows, n_heads, D] of each sequence from position
+    start[b] (0) on (quads_kv_cache_read); given outputs are written in place."""
+    n_seqs, max_pages = _tables(cache, row_off, block_table)
+    if start is not None:
+        _ints(start, torch.int32, (n_seqs,), "start")
+    if out_dtype not in (OUT_BF16, OUT_F32):
+        raise ValueError(f"unknown output dtype {out_dtype}")
+    dt = torch.bfloat16 if out_dtype == OUT_BF16 else torch.float32
+    shape = (rows, cache.n_heads, cache.head_dim)
+    out = []
+    for t, name in ((k_out, "k_out"), (v_out, "v_out")):
+        if t is None:
+            t = _empty(shape, dt, cache.k_codes.device)
+        else:
+            _ints(t, dt, shape, name)
+        out.append(t)
+    _check(load().quads_kv_cache_read(cache.ref, _p(row_off), _p(start), _p(block_table), n_seqs, max_pages, rows,
+                                      _p(out[0]), _p(out[1]), out_dtype, _s()), "quads_kv_cache_read")
+    return out[0], out[1]
+
+
+def _rope(q, k, positions, freq, interleaved, mscale, inverse, q_out, k_out):
+    rows, hq, dim, ld_q = _heads_view(q, "q")
+    hk, ld_k, ld_ko = 0, 0, 0
+    if k is not None:
+        rows_k, hk, dim_k, ld_k = _heads_view(k, "k")
+        if (rows_k, dim_k) != (rows, dim):
+            raise ValueError(f"q and k must have the same rows and head size, got {tuple(q.shape)} and {tuple(k.shape)}")
+        k_out = _empty((rows, hk, dim), torch.bfloat16, k.device) if k_out is None else k_out
+        if k_out.shape != k.shape:
+            raise ValueError("k_out must have k's shape")
+        ld_ko = _heads_view(k_out, "k_out")[3]
+    q_out = _empty((rows, hq, dim), torch.bfloat16, q.device) if q_out is None else q_out
+    if q_out.shape != q.shape:
+        raise ValueError("q_out must have q's shape")
+    ld_qo = _heads_view(q_out, "q_out")[3]
+    _ints(positions, torch.int64, (rows,), "positions")
+    _ints(freq, torch.float64, (freq.numel(),), "freq")
+    _check(load().quads_rope(_p(q), ld_q, hq, _p(k), ld_k, hk, rows, dim, _p(positions), _p(freq), 2 * freq.numel(),
+                             1 if interleaved else 0, float(mscale), 1 if inverse else 0, _p(q_out), ld_qo,
+                             _p(k_out), ld_ko, _s()), "quads_rope")
+    return q_out, k_out
+
+
+def rope(q, k, positions, freq, interleaved=False, mscale=1.0, q_out=None, k_out=None):
+    """Rotary positions of q [rows, heads, D] and k (may be None); freq [rot_dim
+    / 2] float64 radians per position, positions [rows] int64.  Returns
+    (q_out, k_out); the outputs may be the inputs."""
+    return _rope(q, k, positions, freq, interleaved, mscale, False, q_out, k_out)
+
+
+def rope_backward(gq, gk, positions, freq, interleaved=False, mscale=1.0, q_out=None, k_out=None):
+    """Gradients with respect to rope()'s q and k from those with respect to its outputs."""
+    return _rope(gq, gk, positions, freq, interleaved, mscale, True, q_out, k_out)
+
+
+def attention_paged_workspace_bytes(cache, rows, heads_q, n_seqs, max_pages, max_q_len):
+    return int(load().quads_attention_paged_workspace_bytes(cache.ref, rows, heads_q, n_seqs, max_pages, max_q_len))
+
+
+def attention_paged(q, cache, row_off, kv_len, block_table, max_q_len, scale=None, window=0, out=None, lse=None,
+                    ws=None):
+    """Attention of the new tokens' q [rows, heads_q, D] over the paged cache
+    (quads_attention_paged): out [rows, heads_q, D]; lse [rows, heads_q] is
+    filled when given.  scale None: D ** -0.5."""
+    rows, hq, dim, ld_q = _heads_view(q, "q")
+    if dim != cache.head_dim or hq % cache.n_heads:
+        raise ValueError(f"q must be [rows, a multiple of {cache.n_heads}, {cache.head_dim}], got {tuple(q.shape)}")
+    n_seqs, max_pages = _tables(cache, row_off, block_table)
+    _ints(kv_len, torch.int32, (n_seqs,), "kv_len")
+    if out is None:
+        out = _empty((rows, hq, dim), torch.bfloat16, q.device)
+    else:
+        _ints(out, torch.bfloat16, (rows, hq, dim), "out")
+    if lse is not None:
+        _ints(lse, torch.float32, (rows, hq), "lse")
+    if ws is None:
+        n = attention_paged_workspace_bytes(cache, rows, hq, n_seqs, max_pages, max_q_len)
+        ws = _empty((n,), torch.uint8, q.device) if n else None
+    _check(load().quads_attention_paged(
+        _p(q), rows, ld_q, hq, cache.ref, _p(row_off), _p(kv_len), _p(block_table), n_seqs, max_pages, int(max_q_len),
+        dim ** -0.5 if scale is None else float(scale), int(window), _p(out), _p(lse), _p(ws),
+        0 if ws is None else ws.numel() * ws.element_size(), _s()), "quads_attention_paged")
     return out

@@ -1,0 +1,352 @@
+// The paged NVFP4 key/value cache of the rollout: quantized as it is written,
+// read back for the trainer; and the rotary positions of its keys and the
+// queries.
+//
+// [TRACE] "Le problème", "Résultats": the rollout keeps weights, activations
+// and the KV cache in FP4.  A cached value is e2m1 * e4m3 * g on the grid of
+// every other NVFP4 tensor here (blocks of 16 elements of a head, one E4M3
+// scale each), with one decode scale g per key/value head that the caller
+// calibrates, so a token can be written without reading the others.
+#include "kvcache.cuh"
+
+namespace quads {
+
+int check_cache(const quads_kv_cache* c) {
+  QUADS_REQUIRE(c != nullptr, QUADS_ERR_INVALID_ARG, "null cache");
+  QUADS_REQUIRE(c->n_pages >= 0 && c->n_pages < (int64_t(1) << 31), QUADS_ERR_INVALID_ARG,
+                "n_pages must be in [0, 2^31)");
+  QUADS_REQUIRE(c->n_heads >= 1 && c->n_heads <= 1024, QUADS_ERR_UNSUPPORTED_SHAPE, "n_heads must be in [1, 1024]");
+  QUADS_REQUIRE(c->head_dim == 64 || c->head_dim == 128, QUADS_ERR_UNSUPPORTED_SHAPE,
+                "head_dim (%d) must be 64 or 128", c->head_dim);
+  QUADS_REQUIRE(c->page_size >= 16 && c->page_size <= 65536 && c->page_size % 16 == 0, QUADS_ERR_UNSUPPORTED_SHAPE,
+                "page_size (%d) must be a multiple of 16 in [16, 65536]", c->page_size);
+  QUADS_REQUIRE(c->n_pages == 0 || (c->k_codes && c->k_scales && c->v_codes && c->v_scales), QUADS_ERR_INVALID_ARG,
+                "null cache pointer");
+  QUADS_REQUIRE(c->g_k && c->g_v, QUADS_ERR_INVALID_ARG, "null decode scales");
+  QUADS_REQUIRE(aligned(c->k_codes, 16) && aligned(c->k_scales, 16) && aligned(c->v_codes, 16) &&
+                    aligned(c->v_scales, 16),
+                QUADS_ERR_INVALID_ARG, "cache pointers must be 16-byte aligned");
+  return QUADS_OK;
+}
+
+int check_seqs(const int32_t* row_off, const int32_t* block_table, int n_seqs, int max_pages) {
+  QUADS_REQUIRE(n_seqs >= 0 && max_pages >= 0, QUADS_ERR_INVALID_ARG, "n_seqs and max_pages must be >= 0");
+  QUADS_REQUIRE(n_seqs <= 65535, QUADS_ERR_UNSUPPORTED_SHAPE, "n_seqs must be at most 65535");
+  QUADS_REQUIRE(n_seqs == 0 || (row_off && (max_pages == 0 || block_table)), QUADS_ERR_INVALID_ARG, "null pointer");
+  return QUADS_OK;
+}
+
+CacheArgs cache_args(const quads_kv_cache* c, const int32_t* block_table, int n_seqs, int max_pages) {
+  CacheArgs a{};
+  a.k_codes = c->k_codes;
+  a.k_scales = c->k_scales;
+  a.v_codes = c->v_codes;
+  a.v_scales = c->v_scales;
+  a.g_k = c->g_k;
+  a.g_v = c->g_v;
+  a.table = block_table;
+  a.n_pages = c->n_pages;
+  a.page_size = c->page_size;
+  a.n_heads = c->n_heads;
+  a.max_pages = max_pages;
+  a.n_seqs = n_seqs;
+  a.page_div = make_fastdiv(static_cast<uint32_t>(c->page_size));
+  return a;
+}
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxRows = 32;       // rows (tokens) of one CTA
+
+// Rows [r0, r0 + n) of a call: the page and the place in it of each, found by
+// the CTA's warps (row_s[i] = page or -1, at_s[i]).  first(b) is the position
+// of the sequence's first row of this call.
+template <typename First>
+__device__ __forceinline__ void locate_rows(const CacheArgs& c, const int32_t* __restrict__ off, int64_t r0, int n,
+                                            int* page_s, int* at_s, First first) {
+  const int lane = threadIdx.x & 31;
+  for (int i = threadIdx.x >> 5; i < n; i += kThreads / 32) {
+    const int row = static_cast<int>(r0) + i;
+    const int b = warp_find_seq(off, c.n_seqs, row, lane);
+    int page = -1, at = 0;
+    bool in = false;
+    if (b >= 0 && row < __ldg(off + b + 1)) {
+      in = true;
+      const int64_t pos = static_cast<int64_t>(first(b)) + (row - __ldg(off + b));
+      if (pos >= 0 && pos < (int64_t(1) << 31)) page = page_of(c, b, static_cast<int>(pos), at);
+    }
+    if (lane == 0) {
+      page_s[i] = in ? page : -2;                    // -2: behind the last sequence
+      at_s[i] = at;
+    }
+  }
+  __syncthreads();
+}
+
+// --------------------------------------------------------------- the write
+// One thread per block of 16 elements: 32 bytes in, 8 + 1 bytes out.  Bound
+// by HBM: 2 bytes read and 0.5625 written per element.
+__global__ void __launch_bounds__(kThreads) kv_write_kernel(CacheArgs c, const uint16_t* __restrict__ k,
+                                                            const uint16_t* __restrict__ v, int64_t rows,
+                                                            int64_t ld_k, int64_t ld_v, int D,
+                                                            const int32_t* __restrict__ off,
+                                                            const int32_t* __restrict__ kv_len, int per_cta) {
+  __shared__ int page_s[kMaxRows], at_s[kMaxRows];
+  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * per_cta;
+  const int n = static_cast<int>(min(static_cast<int64_t>(per_cta), rows - r0));
+  locate_rows(c, off, r0, n, page_s, at_s,
+              [&](int b) { return __ldg(kv_len + b) - (__ldg(off + b + 1) - __ldg(off + b)); });
+  const int nb = D / 16, per_side = c.n_heads * nb, per_row = 2 * per_side;
+  for (int i = threadIdx.x; i < n * per_row; i += kThreads) {
+    const int r = i / per_row, j = i - r * per_row;
+    const int page = page_s[r];
+    if (page < 0) continue;
+    const bool is_v = j >= per_side;
+    const int jj = is_v ? j - per_side : j;
+    const int head = jj / nb, blk = jj - head * nb;
+    const uint16_t* src = is_v ? v + (r0 + r) * ld_v : k + (r0 + r) * ld_k;
+    uint32_t w[8];
+    load_bf16x16(src + jj * 16, w);
+    const QCore q = quant_core(w, __ldg((is_v ? c.g_v : c.g_k) + head));
+    const int64_t row = cache_row(c, page, head, at_s[r]);
+    *reinterpret_cast<uint2*>((is_v ? c.v_codes : c.k_codes) + row * (D / 2) + blk * 8) = make_uint2(q.lo, q.hi);
+    (is_v ? c.v_scales : c.k_scales)[row * nb + blk] = static_cast<uint8_t>(q.scale);
+  }
+}
+
+// ---------------------------------------------------------------- the read
+// One thread per 16 bytes of output (8 BF16 or 4 FP32 values), so that a
+// warp stores whole lines.  Bound by HBM: 0.5625 bytes read and 2 or 4
+// written per element.
+template <bool kF32>
+__global__ void __launch_bounds__(kThreads) kv_read_kernel(CacheArgs c, void* __restrict__ k_out,
+                                                           void* __restrict__ v_out, int64_t rows, int D,
+                                                           const int32_t* __restrict__ off,
+                                                           const int32_t* __restrict__ start, int per_cta) {
+  constexpr int kVec = kF32 ? 4 : 8;
+  __shared__ int page_s[kMaxRows], at_s[kMaxRows];
+  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * per_cta;
+  const int n = static_cast<int>(min(static_cast<int64_t>(per_cta), rows - r0));
+  locate_rows(c, off, r0, n, page_s, at_s, [&](int b) { return start != nullptr ? __ldg(start + b) : 0; });
+  const int nv = D / kVec, per_side = c.n_heads * nv;
+  const int sides = (k_out != nullptr) + (v_out != nullptr), per_row = sides * per_side;
+  for (int i = threadIdx.x; i < n * per_row; i += kThreads) {
+    const int r = i / per_row, j = i - r * per_row;
+    const int page = page_s[r];
+    if (page == -2) continue;
+    const bool is_v = k_out == nullptr || j >= per_side;
+    const int jj = j >= per_side ? j - per_side : j;
+    const int head = jj / nv, x = (jj - head * nv) * kVec;
+    uint32_t codes = 0, s = 0;
+    if (page >= 0) {
+      const int64_t row = cache_row(c, page, head, at_s[r]);
+      codes = __ldg(reinterpret_cast<const uint32_t*>((is_v ? c.v_codes : c.k_codes) + row * (D / 2) + x / 8 * 4));
+      s = __ldg((is_v ? c.v_scales : c.k_scales) + row * (D / 16) + x / 16);
+    }
+    const float g = __ldg((is_v ? c.g_v : c.g_k) + head), sv = e4m3_value(s);
+    uint32_t h[4];
+    e2m1x8_to_f16x2(codes, h);                         // 8 elements, of which FP32 takes its half
+    if (kF32 && (x & 4)) {
+      h[0] = h[2];
+      h[1] = h[3];
+    }
+    const uint64_t sv2 = pack_f32x2(sv, sv), g2 = pack_f32x2(g, g);
+    uint64_t f[4];                                     // e2m1 * e4m3 is exact, one rounding with g
+#pragma unroll
+    for (int e = 0; e < kVec / 2; ++e) f[e] = fmul2_rn(fmul2_rn(f16x2_to_f32x2(h[e]), sv2), g2);
+    const int64_t o = (r0 + r) * (static_cast<int64_t>(c.n_heads) * D) + head * D + x;
+    void* const out = is_v ? v_out : k_out;
+    if constexpr (kF32)
+      *reinterpret_cast<float4*>(static_cast<float*>(out) + o) =
+          make_float4(lo_f32(f[0]), hi_f32(f[0]), lo_f32(f[1]), hi_f32(f[1]));
+    else
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + o) =
+          make_uint4(f32x2_to_bf16x2(f[0]), f32x2_to_bf16x2(f[1]), f32x2_to_bf16x2(f[2]), f32x2_to_bf16x2(f[3]));
+  }
+}
+
+// -------------------------------------------------------------------- rope
+struct RopeArgs {
+  const uint16_t* q;
+  const uint16_t* k;
+  uint16_t* q_out;
+  uint16_t* k_out;
+  int64_t T, ld_q, ld_k, ld_qo, ld_ko;
+  const int64_t* pos;
+  const double* freq;
+  int hq, hk, D, rot;
+  float mscale, sign;
+};
+
+__device__ __forceinline__ void rotate2(uint32_t a, uint32_t b, const float2 (&cs)[2], uint32_t& ra, uint32_t& rb) {
+  const float a0 = bf16_bits_to_float(a & 0xFFFFu), a1 = bf16_bits_to_float(a >> 16);
+  const float b0 = bf16_bits_to_float(b & 0xFFFFu), b1 = bf16_bits_to_float(b >> 16);
+  ra = pack_bf16x2(a0 * cs[0].x - b0 * cs[0].y, a1 * cs[1].x - b1 * cs[1].y);
+  rb = pack_bf16x2(b0 * cs[0].x + a0 * cs[0].y, b1 * cs[1].x + a1 * cs[1].y);
+}
+
+// A CTA turns `per_cta` tokens: it fills a table of {m cos, m sin} for its
+// tokens (the angle pos * freq in turns, in 64 bits, reduced to [-1/2, 1/2]
+// before it is rounded to 32), then each thread takes 16 elements of a head:
+// 8 pairs.  Bound by HBM: 4 bytes per element, in and out.
+template <bool kInterleaved>
+__global__ void __launch_bounds__(kThreads) rope_kernel(RopeArgs p, int per_cta) {
+  extern __shared__ float2 cs_s[];                     // [per_cta][rot / 2]
+  const int half = p.rot / 2;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * per_cta;
+  const int n = static_cast<int>(min(static_cast<int64_t>(per_cta), p.T - t0));
+  for (int i = threadIdx.x; i < n * half; i += kThreads) {
+    const int t = i / half, f = i - t * half;
+    double turns = static_cast<double>(__ldg(reinterpret_cast<const long long*>(p.pos) + t0 + t)) *
+                   (__ldg(p.freq + f) * 0.15915494309189533577);
+    turns -= rint(turns);
+    float s, c;
+    sincospif(2.0f * static_cast<float>(turns), &s, &c);
+    cs_s[i] = make_float2(p.mscale * c, p.sign * (p.mscale * s));
+  }
+  __syncthreads();
+  const int nv = p.D / 16, per_row = (p.hq + p.hk) * nv;
+  for (int i = threadIdx.x; i < n * per_row; i += kThreads) {
+    const int t = i / per_row, j = i - t * per_row;
+    int head = j / nv;
+    const int x = j - head * nv;
+    const bool is_k = head >= p.hq;
+    if (is_k) head -= p.hq;
+    const uint16_t* src = (is_k ? p.k + (t0 + t) * p.ld_k : p.q + (t0 + t) * p.ld_q) + head * p.D;
+    uint16_t* dst = (is_k ? p.k_out + (t0 + t) * p.ld_ko : p.q_out + (t0 + t) * p.ld_qo) + head * p.D;
+    // the thread's two groups of 8 elements: both of its pairs' sides in the
+    // half layout, 16 neighbours in the interleaved one and past rot
+    const bool turned = x < p.rot / 16;
+    const int e0 = (!kInterleaved && turned) ? 8 * x : 16 * x;
+    const int e1 = (!kInterleaved && turned) ? half + 8 * x : 16 * x + 8;
+    const uint4 a = *reinterpret_cast<const uint4*>(src + e0);       // plain loads: out may be in
+    const uint4 b = *reinterpret_cast<const uint4*>(src + e1);
+    uint32_t u[4] = {a.x, a.y, a.z, a.w}, w[4] = {b.x, b.y, b.z, b.w};
+    if (turned) {
+      const float2* cs = cs_s + t * half + 8 * x;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if constexpr (kInterleaved) {                  // one pair per word
+          uint32_t* const g = e < 2 ? u + 2 * e : w + 2 * (e - 2);
+          const float2 c2[2] = {cs[2 * e], cs[2 * e + 1]};
+          uint32_t ra, rb;
+          rotate2(__byte_perm(g[0], g[1], 0x5410), __byte_perm(g[0], g[1], 0x7632), c2, ra, rb);
+          g[0] = __byte_perm(ra, rb, 0x5410);
+          g[1] = __byte_perm(ra, rb, 0x7632);
+        } else {
+          const float2 c2[2] = {cs[2 * e], cs[2 * e + 1]};
+          rotate2(u[e], w[e], c2, u[e], w[e]);
+        }
+      }
+    }
+    *reinterpret_cast<uint4*>(dst + e0) = make_uint4(u[0], u[1], u[2], u[3]);
+    *reinterpret_cast<uint4*>(dst + e1) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// Rows of a CTA: as many as keep `want` items of work, fewer where the call
+// is too small to give every SM four CTAs.
+int rows_per_cta(int64_t rows, int per_row, int want) {
+  int64_t n = want / (per_row > 0 ? per_row : 1);
+  const int64_t spread = ceil_div(rows, int64_t(4) * num_sms());
+  if (n > spread) n = spread;
+  if (n > kMaxRows) n = kMaxRows;
+  return static_cast<int>(n < 1 ? 1 : n);
+}
+
+}  // namespace
+}  // namespace quads
+
+using namespace quads;
+
+extern "C" {
+
+int quads_kv_cache_write(const quads_kv_cache* cache, const uint16_t* k, const uint16_t* v, int64_t rows, int64_t ld_k,
+                         int64_t ld_v, const int32_t* row_off, const int32_t* kv_len, const int32_t* block_table,
+                         int n_seqs, int max_pages, quads_stream_t stream) {
+  clear_error();
+  QUADS_TRY(check_cache(cache));
+  QUADS_TRY(check_seqs(row_off, block_table, n_seqs, max_pages));
+  const int64_t width = static_cast<int64_t>(cache->n_heads) * cache->head_dim;
+  QUADS_REQUIRE(rows >= 0 && rows < (int64_t(1) << 31), QUADS_ERR_INVALID_ARG, "rows must be in [0, 2^31)");
+  QUADS_REQUIRE(ld_k >= width && ld_v >= width && ld_k % 8 == 0 && ld_v % 8 == 0, QUADS_ERR_INVALID_ARG,
+                "row strides must be multiples of 8 of at least n_heads * head_dim");
+  if (rows == 0 || n_seqs == 0 || max_pages == 0 || cache->n_pages == 0) return QUADS_OK;
+  QUADS_REQUIRE(k && v && kv_len, QUADS_ERR_INVALID_ARG, "null pointer");
+  QUADS_REQUIRE(aligned(k, 16) && aligned(v, 16), QUADS_ERR_INVALID_ARG, "k and v must be 16-byte aligned");
+  const CacheArgs c = cache_args(cache, block_table, n_seqs, max_pages);
+  const int per = rows_per_cta(rows, static_cast<int>(width / 8), 1024);
+  kv_write_kernel<<<static_cast<unsigned>(ceil_div(rows, int64_t(per))), kThreads, 0, stream>>>(
+      c, k, v, rows, ld_k, ld_v, cache->head_dim, row_off, kv_len, per);
+  count_launches(1);
+  return check_launch("kv_write_kernel");
+}
+
+int quads_kv_cache_read(const quads_kv_cache* cache, const int32_t* row_off, const int32_t* start,
+                        const int32_t* block_table, int n_seqs, int max_pages, int64_t rows, void* k_out, void* v_out,
+                        int out_dtype, quads_stream_t stream) {
+  clear_error();
+  QUADS_TRY(check_cache(cache));
+  QUADS_TRY(check_seqs(row_off, block_table, n_seqs, max_pages));
+  QUADS_REQUIRE(rows >= 0 && rows < (int64_t(1) << 31), QUADS_ERR_INVALID_ARG, "rows must be in [0, 2^31)");
+  QUADS_REQUIRE(out_dtype == QUADS_OUT_BF16 || out_dtype == QUADS_OUT_F32, QUADS_ERR_INVALID_ARG,
+                "unknown output dtype %d", out_dtype);
+  if (rows == 0 || n_seqs == 0) return QUADS_OK;
+  QUADS_REQUIRE(k_out || v_out, QUADS_ERR_INVALID_ARG, "no output");
+  QUADS_REQUIRE(aligned(k_out, 16) && aligned(v_out, 16), QUADS_ERR_INVALID_ARG, "outputs must be 16-byte aligned");
+  const CacheArgs c = cache_args(cache, block_table, n_seqs, max_pages);
+  const bool f32 = out_dtype == QUADS_OUT_F32;
+  const int per_row = cache->n_heads * cache->head_dim / (f32 ? 4 : 8) * ((k_out != nullptr) + (v_out != nullptr));
+  const int per = rows_per_cta(rows, per_row, 4096);
+  const unsigned grid = static_cast<unsigned>(ceil_div(rows, int64_t(per)));
+  if (f32)
+    kv_read_kernel<true><<<grid, kThreads, 0, stream>>>(c, k_out, v_out, rows, cache->head_dim, row_off, start, per);
+  else
+    kv_read_kernel<false><<<grid, kThreads, 0, stream>>>(c, k_out, v_out, rows, cache->head_dim, row_off, start, per);
+  count_launches(1);
+  return check_launch("kv_read_kernel");
+}
+
+int quads_rope(const uint16_t* q, int64_t ld_q, int heads_q, const uint16_t* k, int64_t ld_k, int heads_k, int64_t T,
+               int head_dim, const int64_t* positions, const double* freq, int rot_dim, int interleaved, float mscale,
+               int inverse, uint16_t* q_out, int64_t ld_q_out, uint16_t* k_out, int64_t ld_k_out,
+               quads_stream_t stream) {
+  clear_error();
+  QUADS_REQUIRE(T >= 0 && T < (int64_t(1) << 31), QUADS_ERR_INVALID_ARG, "T must be in [0, 2^31)");
+  QUADS_REQUIRE(heads_q >= 0 && heads_k >= 0 && heads_q + heads_k >= 1 && heads_q <= 4096 && heads_k <= 4096,
+                QUADS_ERR_INVALID_ARG, "1 to 4096 heads of each kind");
+  QUADS_REQUIRE(head_dim >= 16 && head_dim <= 1024 && head_dim % 16 == 0, QUADS_ERR_UNSUPPORTED_SHAPE,
+                "head_dim (%d) must be a multiple of 16 in [16, 1024]", head_dim);
+  QUADS_REQUIRE(rot_dim >= 16 && rot_dim <= head_dim && rot_dim % 16 == 0, QUADS_ERR_UNSUPPORTED_SHAPE,
+                "rot_dim (%d) must be a multiple of 16 in [16, head_dim]", rot_dim);
+  const int64_t wq = static_cast<int64_t>(heads_q) * head_dim, wk = static_cast<int64_t>(heads_k) * head_dim;
+  QUADS_REQUIRE(heads_q == 0 || (ld_q >= wq && ld_q_out >= wq && ld_q % 8 == 0 && ld_q_out % 8 == 0),
+                QUADS_ERR_INVALID_ARG, "q's row strides must be multiples of 8 of at least heads_q * head_dim");
+  QUADS_REQUIRE(heads_k == 0 || (ld_k >= wk && ld_k_out >= wk && ld_k % 8 == 0 && ld_k_out % 8 == 0),
+                QUADS_ERR_INVALID_ARG, "k's row strides must be multiples of 8 of at least heads_k * head_dim");
+  if (T == 0) return QUADS_OK;
+  QUADS_REQUIRE((heads_q == 0 || (q && q_out)) && (heads_k == 0 || (k && k_out)) && positions && freq,
+                QUADS_ERR_INVALID_ARG, "null pointer");
+  QUADS_REQUIRE(aligned(q, 16) && aligned(k, 16) && aligned(q_out, 16) && aligned(k_out, 16) && aligned(positions, 8) &&
+                    aligned(freq, 8),
+                QUADS_ERR_INVALID_ARG, "q, k and the outputs must be 16-byte aligned");
+  RopeArgs p{};
+  p.q = q; p.k = k; p.q_out = q_out; p.k_out = k_out;
+  p.T = T; p.ld_q = ld_q; p.ld_k = ld_k; p.ld_qo = ld_q_out; p.ld_ko = ld_k_out;
+  p.pos = positions; p.freq = freq;
+  p.hq = heads_q; p.hk = heads_k; p.D = head_dim; p.rot = rot_dim;
+  p.mscale = mscale; p.sign = inverse ? -1.0f : 1.0f;
+  int per = rows_per_cta(T, (heads_q + heads_k) * head_dim / 16, 1024);
+  per = per < 12288 / rot_dim ? per : 12288 / rot_dim;                               // table of at most 48 KB
+  const size_t smem = static_cast<size_t>(per) * (rot_dim / 2) * sizeof(float2);
+  const unsigned grid = static_cast<unsigned>(ceil_div(T, int64_t(per)));
+  if (interleaved)
+    rope_kernel<true><<<grid, kThreads, smem, stream>>>(p, per);
+  else
+    rope_kernel<false><<<grid, kThreads, smem, stream>>>(p, per);
+  count_launches(1);
+  return check_launch("rope_kernel");
+}
+
+}  // extern "C"
