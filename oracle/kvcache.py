@@ -75,12 +75,12 @@ def read(cache, row_off, table, start=None):
 def attention(q, cache, row_off, kv_len, table, scale, window=0):
     """By the definition, over the positions with a page up to a row's own and
     inside the window: out [rows, heads_q, D], lse [rows, heads_q], and what
-    error bounds need: vabs, the softmax average of |v|, and sabs, the largest
-    scale * sum |q_i k_i| of a row."""
+    error bounds need: vabs, the softmax average of |v|, sabs, the largest scale *
+    sum |q_i k_i| of a row, and vsum, the plain sum of |v|."""
     rows, hq, D = q.shape
     heads = cache["k_codes"].shape[1]
     out, lse, vabs = np.zeros((rows, hq, D)), np.full((rows, hq), -np.inf), np.zeros((rows, hq, D))
-    sabs = np.zeros((rows, hq))
+    sabs, vsum = np.zeros((rows, hq)), np.zeros((rows, hq, D))
     memo = {}
     for r, (b, pos) in enumerate(row_positions(row_off, kv_len)):
         js = [j for j in range(max(0, pos - window + 1) if window else 0, pos + 1)
@@ -102,7 +102,8 @@ def attention(q, cache, row_off, kv_len, table, scale, window=0):
                 vabs[r, i] = e @ np.abs(v) / e.sum()
                 lse[r, i] = m + np.log(e.sum())
                 sabs[r, i] = (np.abs(k) @ np.abs(q[r, i])).max() * abs(scale)
-    return out, lse, vabs, sabs
+                vsum[r, i] = np.abs(v).sum(0)
+    return out, lse, vabs, sabs, vsum
 
 
 def rope(x, positions, freq, interleaved=False, mscale=1.0, inverse=False):

@@ -57,13 +57,13 @@ def values64(t, name):
 
 
 def attention64(q, t, row_off, kv_len, table, scale, window=0):
-    """out, lse, vabs, sabs as oracle.kvcache.attention gives them, in float64 torch."""
+    """out, lse, vabs, sabs, vsum as oracle.kvcache.attention gives them, in float64 torch."""
     dev, (rows, hq, D) = q.device, q.shape
     n_pages, hk, ps, _ = t["k_codes"].shape
     kd, vd = values64(t, "k"), values64(t, "v")
     f = lambda *s: torch.zeros(*s, dtype=torch.float64, device=dev)
-    out, vabs, sabs, lse = f(rows, hq, D), f(rows, hq, D), f(rows, hq), torch.full((rows, hq), -math.inf,
-                                                                                 dtype=torch.float64, device=dev)
+    out, vabs, vsum, sabs = f(rows, hq, D), f(rows, hq, D), f(rows, hq, D), f(rows, hq)
+    lse = torch.full((rows, hq), -math.inf, dtype=torch.float64, device=dev)
     off, lens, tab = row_off.tolist(), kv_len.tolist(), table.cpu()
     for b, length in enumerate(lens):
         n = off[b + 1] - off[b]
@@ -93,13 +93,14 @@ def attention64(q, t, row_off, kv_len, table, scale, window=0):
             w = e / l[..., None]
             out[rr] = torch.einsum("nhl,lhd->nhd", w, v)
             vabs[rr] = torch.einsum("nhl,lhd->nhd", w, v.abs())
+            vsum[rr] = torch.einsum("nl,lhd->nhd", see.double(), v.abs())
             lse[rr] = torch.where(any_, m + torch.log(l), -math.inf)
             a = torch.einsum("nhd,lhd->nhl", qq.abs(), k.abs()) * abs(scale)
             sabs[rr] = a.masked_fill(~see[:, None], 0.0).amax(-1)
-    return out, lse, vabs, sabs
+    return out, lse, vabs, sabs, vsum
 
 
-def attention_bounds(out, lse, vabs, sabs, dim):
+def attention_bounds(out, lse, vabs, sabs, vsum, dim):
     """Elementwise bounds on a kernel's out (BF16) and lse (FP32).
 
     A score is a sum of dim products of exact factors, each of at most dim
@@ -108,8 +109,12 @@ def attention_bounds(out, lse, vabs, sabs, dim):
     its scaling.  A weight rounded to 16 bits is off by 2^-11 (FP16), its
     exponential by 2^-21, the average of the scores' errors by 2 d; all of
     that times the weighted |v|.  Sums of n weights in 32 bits add 2^-16 at
-    most here.  The result is rounded to BF16: 2^-8 of it."""
+    most here.  FP16's steps do not shrink below 2^-24: with weights held at
+    2^7 times their share of a maximum that some key attains, each is off by
+    at most 2^-25 / 2^7 = 2^-32 of a sum that is at least that maximum's.  The
+    result is rounded to BF16: 2^-8 of it."""
     d = sabs * (dim * 2.0 ** -23 + 2.0 ** -22)
-    tol = 2.0 ** -8 * out.abs() + (2.0 ** -11 + 2.0 ** -15 + 2 * d[..., None]) * vabs * (1 + 2.0 ** -7) + 1e-30
+    tol = 2.0 ** -8 * out.abs() + (2.0 ** -11 + 2.0 ** -15 + 2 * d[..., None]) * vabs * (1 + 2.0 ** -7) + \
+        2.0 ** -32 * vsum * (1 + 2.0 ** -7) + 1e-30
     tol_lse = d + 2.0 ** -16 + 2.0 ** -22 * torch.where(torch.isfinite(lse), lse.abs(), torch.zeros_like(lse))
     return tol, tol_lse

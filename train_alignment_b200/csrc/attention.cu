@@ -4,24 +4,11 @@
 //
 // One warp per (row, query head): an online softmax over the positions in
 // order, 32 positions' scores at a time.
-#include <math_constants.h>
-
-#include "kvcache.cuh"
+#include "attention.cuh"
+#include "attention_decode.cuh"
 
 namespace quads {
 namespace {
-
-struct AttnArgs {
-  CacheArgs c;
-  const uint16_t* q;
-  uint16_t* out;
-  float* lse;
-  const int32_t* off;
-  const int32_t* kv_len;
-  int64_t rows, ld_q;
-  int hq, group, max_q, window;
-  float scale;
-};
 
 template <int D>
 __global__ void __launch_bounds__(128) attention_kernel(AttnArgs p) {
@@ -76,6 +63,38 @@ __global__ void __launch_bounds__(128) attention_kernel(AttnArgs p) {
   if (p.lse != nullptr && lane == 0) p.lse[r * p.hq + h] = l > 0.0f ? m + logf(l) : -CUDART_INF_F;
 }
 
+// CTAs of the kernel for few rows: as many as are resident at once.
+int dec_grid(int nt) { return (nt == 1 ? 4 : 3) * num_sms(); }
+constexpr int kDecMinQuota = 4;      // tiles of a run: shorter ones cost more in joining than they save
+
+size_t dec_workspace(int D, int nt) {
+  return static_cast<size_t>(2) * dec_grid(nt) * (8 * nt) * (D * sizeof(float) + sizeof(float2));
+}
+
+template <int D, int NT>
+int launch_decode(AttnArgs p, void* ws, int unit_rows, cudaStream_t stream) {
+  const int grid = dec_grid(NT);
+  p.part_o = static_cast<float*>(ws);
+  p.part_ml = reinterpret_cast<float2*>(p.part_o + static_cast<size_t>(2) * grid * (8 * NT) * D);
+  attention_decode_kernel<D, NT><<<grid, kDecThreads, 0, stream>>>(p, kDecMinQuota);
+  QUADS_TRY(check_launch("attention_decode_kernel"));
+  // the joining kernel is resident before the last run ends and waits for it
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  // rows on blocks of their own where few units are cut into many runs
+  cfg.gridDim = dim3(grid - 1, static_cast<int64_t>(p.c.n_seqs) * p.c.n_heads * 8 <= grid ? unit_rows : 1);
+  cfg.blockDim = dim3(4 * D);
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, attention_combine_kernel<D, NT>, p, grid, kDecMinQuota) != cudaSuccess)
+    return check_launch("attention_combine_kernel");
+  count_launches(2);
+  return QUADS_OK;
+}
+
 }  // namespace
 }  // namespace quads
 
@@ -85,7 +104,10 @@ extern "C" {
 
 size_t quads_attention_paged_workspace_bytes(const quads_kv_cache* cache, int64_t rows, int heads_q, int n_seqs,
                                              int max_pages, int max_q_len) {
-  (void)cache; (void)rows; (void)heads_q; (void)n_seqs; (void)max_pages; (void)max_q_len;
+  if (cache == nullptr || cache->n_heads < 1 || heads_q < 1 || heads_q % cache->n_heads != 0) return 0;
+  (void)rows; (void)n_seqs; (void)max_pages;
+  const int64_t unit_rows = static_cast<int64_t>(max_q_len) * (heads_q / cache->n_heads);
+  if (unit_rows <= 16) return dec_workspace(cache->head_dim, unit_rows <= 8 ? 1 : 2);
   return 0;
 }
 
@@ -96,7 +118,7 @@ int quads_attention_paged(const uint16_t* q, int64_t rows, int64_t ld_q, int hea
   clear_error();
   QUADS_TRY(check_cache(cache));
   QUADS_TRY(check_seqs(row_off, block_table, n_seqs, max_pages));
-  QUADS_REQUIRE(rows >= 0 && rows < (int64_t(1) << 31), QUADS_ERR_INVALID_ARG, "rows must be in [0, 2^31)");
+  QUADS_REQUIRE(rows >= 0 && rows < (int64_t(1) << 30), QUADS_ERR_INVALID_ARG, "rows must be in [0, 2^30)");
   QUADS_REQUIRE(heads_q >= 1 && heads_q <= 4096 && heads_q % cache->n_heads == 0, QUADS_ERR_UNSUPPORTED_SHAPE,
                 "heads_q (%d) must be a multiple of the cache's %d heads, at most 4096", heads_q, cache->n_heads);
   QUADS_REQUIRE(ld_q >= static_cast<int64_t>(heads_q) * cache->head_dim && ld_q % 8 == 0, QUADS_ERR_INVALID_ARG,
@@ -106,12 +128,22 @@ int quads_attention_paged(const uint16_t* q, int64_t rows, int64_t ld_q, int hea
   if (rows == 0 || n_seqs == 0 || max_q_len == 0) return QUADS_OK;
   QUADS_REQUIRE(q && out && kv_len, QUADS_ERR_INVALID_ARG, "null pointer");
   QUADS_REQUIRE(aligned(q, 16) && aligned(out, 16), QUADS_ERR_INVALID_ARG, "q and out must be 16-byte aligned");
-  (void)ws; (void)ws_bytes;
+  const size_t need = quads_attention_paged_workspace_bytes(cache, rows, heads_q, n_seqs, max_pages, max_q_len);
+  QUADS_REQUIRE(need == 0 || (ws != nullptr && ws_bytes >= need && aligned(ws, 16)), QUADS_ERR_INVALID_ARG,
+                "a 16-byte aligned workspace of %zu bytes is required", need);
   AttnArgs p{};
   p.c = cache_args(cache, block_table, n_seqs, max_pages);
   p.q = q; p.out = out; p.lse = lse; p.off = row_off; p.kv_len = kv_len;
   p.rows = rows; p.ld_q = ld_q; p.hq = heads_q; p.group = heads_q / cache->n_heads;
-  p.max_q = max_q_len; p.window = window; p.scale = scale;
+  p.max_q = max_q_len; p.window = window < (1 << 30) ? window : (1 << 30); p.scale = scale;
+  p.group_div = make_fastdiv(static_cast<uint32_t>(p.group));
+  const int64_t unit_rows = static_cast<int64_t>(max_q_len) * p.group;
+  if (unit_rows <= 16) {
+    const int n = static_cast<int>(unit_rows);
+    if (cache->head_dim == 64)
+      return n <= 8 ? launch_decode<64, 1>(p, ws, n, stream) : launch_decode<64, 2>(p, ws, n, stream);
+    return n <= 8 ? launch_decode<128, 1>(p, ws, n, stream) : launch_decode<128, 2>(p, ws, n, stream);
+  }
   const unsigned grid = static_cast<unsigned>(ceil_div(rows * heads_q, int64_t(4)));
   if (cache->head_dim == 64)
     attention_kernel<64><<<grid, 128, 0, stream>>>(p);

@@ -1,0 +1,100 @@
+// What the attention kernels share (internal).
+#pragma once
+
+#include <math_constants.h>
+
+#include "kvcache.cuh"
+
+namespace quads {
+
+struct AttnArgs {
+  CacheArgs c;
+  const uint16_t* q;
+  uint16_t* out;
+  float* lse;               // nullable
+  const int32_t* off;
+  const int32_t* kv_len;
+  int64_t rows, ld_q;
+  int hq, group, max_q, window;
+  float scale;
+  FastDiv group_div;
+  // partial results of units whose keys are split: per slot kRows rows of D
+  // unnormalised sums, and {maximum, sum} of each row
+  float* part_o;
+  float2* part_ml;
+};
+
+// A sequence of a call: its rows, and the keys that they can see.
+struct SeqInfo {
+  int r0;      // first row
+  int nq;      // rows that are computed
+  int pos0;    // position of the first row (may be negative)
+  int lo, hi;  // keys [lo, hi), lo a multiple of 16
+};
+
+__device__ __forceinline__ SeqInfo seq_info(const AttnArgs& p, int b) {
+  const int rows = static_cast<int>(p.rows);
+  const int r0 = min(max(__ldg(p.off + b), 0), rows), r1 = min(max(__ldg(p.off + b + 1), r0), rows);
+  SeqInfo s;
+  s.r0 = r0;
+  const int n = r1 - r0;
+  s.nq = min(n, p.max_q);
+  const int64_t pos0 = static_cast<int64_t>(max(__ldg(p.kv_len + b), 0)) - n;      // > -2^30: rows < 2^30
+  s.pos0 = static_cast<int>(pos0);
+  const int64_t cap = static_cast<int64_t>(p.c.max_pages) * p.c.page_size;
+  s.hi = static_cast<int>(max(int64_t(0), min(cap, pos0 + s.nq)));
+  int64_t lo = p.window > 0 ? pos0 - p.window + 1 : 0;
+  lo = min(max(lo, int64_t(0)), static_cast<int64_t>(s.hi));
+  s.lo = static_cast<int>(lo) & ~15;
+  return s;
+}
+
+// Queries are multiplied as 16-bit floats with 11 significant bits: a row is
+// scaled by a power of two that brings its largest element to [1, 2), which
+// keeps every BF16 element down to 2^-17 of the largest exact (smaller ones
+// are off by 2^-25 of the largest).  Returns the row's exponent field.
+__device__ __forceinline__ uint32_t row_exponent(uint32_t max_bf16_bits) {
+  const uint32_t e = (max_bf16_bits >> 7) & 0xFFu;
+  return min(max(e, 1u), 253u);
+}
+__device__ __forceinline__ float exp_field_up(uint32_t e) { return __uint_as_float(e << 23); }              // 2^(e - 127)
+__device__ __forceinline__ float exp_field_down(uint32_t e) { return __uint_as_float((254u - e) << 23); }   // 2^(127 - e)
+
+// Two BF16 (a word) times r -> two FP16.
+__device__ __forceinline__ uint32_t bf16x2_scaled_f16x2(uint32_t w, float r) {
+  uint32_t o;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(o) : "f"(__uint_as_float(w & 0xFFFF0000u) * r), "f"(__uint_as_float(w << 16) * r));
+  return o;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t o;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(o) : "f"(hi), "f"(lo));
+  return o;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// An E4M3 scale as {v, v} FP16 with v = val(s) * 2^-8: the code shifted into
+// FP16's exponent and mantissa (bias 15 instead of 7; subnormals alike).  No
+// code gives a NaN or an infinity (0x7F gives 480 * 2^-8), so bytes of places
+// that nothing was written to cannot pass through a weight of zero.
+__device__ __forceinline__ uint32_t scale_f16x2(uint32_t s) { return (s & 0x7Fu) * 0x00800080u; }
+// Two such scales.
+__device__ __forceinline__ uint32_t scale_pair_f16x2(uint32_t s0, uint32_t s1) {
+  return ((s0 & 0x7Fu) << 7) | ((s1 & 0x7Fu) << 23);
+}
+constexpr float kScaleUnit = 256.0f;      // what the 2^-8 above is undone with
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+// A row's running maximum may fall this far (in powers of two) behind a new
+// score before its sums are rescaled; weights are kept at 2^kShift times
+// their value so that FP16 holds them from 2^-31 (2^-21 as a normal number)
+// to 2^15 of the maximum's.
+constexpr float kLag = 8.0f;
+constexpr float kShift = 7.0f;
+
+}  // namespace quads

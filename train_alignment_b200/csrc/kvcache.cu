@@ -73,7 +73,7 @@ __device__ __forceinline__ void locate_rows(const CacheArgs& c, const int32_t* _
     bool in = false;
     if (b >= 0 && row < __ldg(off + b + 1)) {
       in = true;
-      const int64_t pos = static_cast<int64_t>(first(b)) + (row - __ldg(off + b));
+      const int64_t pos = first(b) + (row - __ldg(off + b));
       if (pos >= 0 && pos < (int64_t(1) << 31)) page = page_of(c, b, static_cast<int>(pos), at);
     }
     if (lane == 0) {
@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(CacheArgs c, const u
   const int64_t r0 = static_cast<int64_t>(blockIdx.x) * per_cta;
   const int n = static_cast<int>(min(static_cast<int64_t>(per_cta), rows - r0));
   locate_rows(c, off, r0, n, page_s, at_s,
-              [&](int b) { return __ldg(kv_len + b) - (__ldg(off + b + 1) - __ldg(off + b)); });
+              [&](int b) { return static_cast<int64_t>(__ldg(kv_len + b)) - (__ldg(off + b + 1) - __ldg(off + b)); });
   const int nb = D / 16, per_side = c.n_heads * nb, per_row = 2 * per_side;
   for (int i = threadIdx.x; i < n * per_row; i += kThreads) {
     const int r = i / per_row, j = i - r * per_row;
@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(CacheArgs c, void* __
   __shared__ int page_s[kMaxRows], at_s[kMaxRows];
   const int64_t r0 = static_cast<int64_t>(blockIdx.x) * per_cta;
   const int n = static_cast<int>(min(static_cast<int64_t>(per_cta), rows - r0));
-  locate_rows(c, off, r0, n, page_s, at_s, [&](int b) { return start != nullptr ? __ldg(start + b) : 0; });
+  locate_rows(c, off, r0, n, page_s, at_s, [&](int b) -> int64_t { return start != nullptr ? __ldg(start + b) : 0; });
   const int nv = D / kVec, per_side = c.n_heads * nv;
   const int sides = (k_out != nullptr) + (v_out != nullptr), per_row = sides * per_side;
   for (int i = threadIdx.x; i < n * per_row; i += kThreads) {
