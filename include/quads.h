@@ -598,14 +598,14 @@ int trace_replay_direction(const uint8_t* bits, const uint8_t* scales, int scale
  * A cache holds n_pages pages of page_size tokens for n_heads key/value
  * heads of head_dim elements, keys and values alike:
  *   codes  [n_pages][n_heads][page_size][head_dim / 2], packed E2M1;
- *   scales [n_pages][n_heads][page_size][head_dim / 16], E4M3, one per 16
- *          consecutive elements of a head (the sign bit is not read);
+ *   scales [n_pages][n_heads][page_size][head_dim / 16], E4M3 (0 to
+ *          0x7E), one per 16 consecutive elements of a head;
  *   g      device float[n_heads]: the decode scale of each head, given by the
  *          caller (calibrated: max |k| of the head / 2688) and fixed while
  *          tokens written with it are in use.
  * value = e2m1 * e4m3 * g.  head_dim is 64 or 128, page_size a multiple of
- * 16 up to 65536, n_heads at most 1024, n_pages < 2^31; the four arrays
- * 16-byte aligned.
+ * 16 up to 65536, n_heads at most 1024, n_pages < 2^31, their product below
+ * 2^32 - 1; the four arrays 16-byte aligned.
  *
  * Sequences (all device int32): row_off [n_seqs + 1], ascending from 0: rows
  * row_off[b] .. row_off[b + 1] - 1 of a call belong to sequence b, rows behind

@@ -19,19 +19,16 @@ class KVCache:
     Wraps the given tensors; KVCache.empty allocates them."""
 
     def __init__(self, k_codes, k_scales, v_codes, v_scales, g_k, g_v):
-        n_pages, n_heads, page_size, half = k_codes.shape
+        n_pages, n_heads, page_size, half = codes = k_codes.shape
+        scales, heads, dev = (n_pages, n_heads, page_size, half // 8), (n_heads,), k_codes.get_device()
+        u8, f32 = torch.uint8, torch.float32
+        for t, dt, shape, name in ((k_codes, u8, codes, "k_codes"), (v_codes, u8, codes, "v_codes"),
+                                   (k_scales, u8, scales, "k_scales"), (v_scales, u8, scales, "v_scales"),
+                                   (g_k, f32, heads, "g_k"), (g_v, f32, heads, "g_v")):
+            if t.dtype is not dt or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
+                raise ValueError(f"{name} must be a contiguous {dt} tensor of shape {tuple(shape)} on {k_codes.device}, "
+                                 f"got {t.dtype} {tuple(t.shape)} on {t.device}")
         self.n_pages, self.n_heads, self.page_size, self.head_dim = n_pages, n_heads, page_size, 2 * half
-        scales = (n_pages, n_heads, page_size, half // 8)
-        for t, dt, shape, name in ((k_codes, torch.uint8, (n_pages, n_heads, page_size, half), "k_codes"),
-                                   (v_codes, torch.uint8, (n_pages, n_heads, page_size, half), "v_codes"),
-                                   (k_scales, torch.uint8, scales, "k_scales"),
-                                   (v_scales, torch.uint8, scales, "v_scales"),
-                                   (g_k, torch.float32, (n_heads,), "g_k"), (g_v, torch.float32, (n_heads,), "g_v")):
-            if t.dtype != dt or tuple(t.shape) != shape or not t.is_contiguous():
-                raise ValueError(f"{name} must be a contiguous {dt} tensor of shape {shape}, got {t.dtype} "
-                                 f"{tuple(t.shape)}")
-            if t.device != k_codes.device:
-                raise ValueError(f"{name} is on {t.device}, k_codes on {k_codes.device}")
         self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
         self.g_k, self.g_v = g_k, g_v
         self.desc = B.KVCacheDesc(n_pages, page_size, n_heads, 2 * half, 0, k_codes.data_ptr(), k_scales.data_ptr(),

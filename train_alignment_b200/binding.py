@@ -690,101 +690,118 @@ def residual_add(x, y, out=None):
 
 
 # ------------------------------------------------ KV cache, rope, attention
+#
+# These calls are made once per layer and decoding step, where the host's time
+# is the call's time: the checks are written out, and pointers and the stream
+# are passed as plain integers.
 
 
-def _here(t, name):
-    """A CUDA tensor of the current device (the one the call's stream and
-    launches belong to)."""
-    if not t.is_cuda:
+def _stream(t, name):
+    """Raw current stream of t's device, which must be the current one (the
+    device the launches go to)."""
+    d = t.get_device()
+    if d < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, not on the current device cuda:{torch.cuda.current_device()}")
+    if d != torch.cuda.current_device():
+        raise ValueError(f"{name} is on cuda:{d}, not on the current device cuda:{torch.cuda.current_device()}")
+    return torch._C._cuda_getCurrentRawStream(d)
 
 
-def _ints(t, dtype, shape, name):
-    _here(t, name)
-    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape}, got {t.dtype} {tuple(t.shape)}")
+def _like(t, first, dtype, shape, name):
+    """t's pointer, after checking that it is a contiguous tensor of that type
+    and shape on the device of `first`."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != first.get_device():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {first.device}, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
 
 
-def _heads_view(x, name):
-    """A BF16 tensor [rows, heads, dim] whose rows may be strided: (rows, heads, dim, row stride)."""
-    _here(x, name)
-    if x.dtype != torch.bfloat16 or x.dim() != 3:
+def _heads_view(x, first, name):
+    """A BF16 tensor [rows, heads, dim] on the device of `first` whose rows may
+    be strided: (rows, heads, dim, row stride)."""
+    if x.dtype is not torch.bfloat16 or x.dim() != 3:
         raise ValueError(f"{name} must be a bfloat16 tensor [rows, heads, dim]")
+    if x.get_device() != first.get_device():
+        raise ValueError(f"{name} is on {x.device}, not on {first.device}")
     rows, heads, dim = x.shape
-    if (x.stride(2) != 1 and dim > 1) or (x.stride(1) != dim and heads > 1):
+    ld, sh, sd = x.stride()
+    if (sd != 1 and dim > 1) or (sh != dim and heads > 1):
         raise ValueError(f"{name}: the heads of a row must be contiguous")
-    ld = x.stride(0) if rows > 1 else heads * dim
-    return rows, heads, dim, ld
+    return rows, heads, dim, (ld if rows > 1 else heads * dim)
 
 
 def _tables(cache, row_off, block_table):
-    """Checks the cache's device, row_off and block_table; (n_seqs, max_pages)."""
-    _here(cache.k_codes, "the cache")
+    """Checks row_off and block_table: (n_seqs, max_pages, their pointers)."""
     if block_table.dim() != 2:
         raise ValueError("block_table must be [n_seqs, max_pages]")
-    n_seqs, max_pages = block_table.shape
-    _ints(block_table, torch.int32, (n_seqs, max_pages), "block_table")
-    _ints(row_off, torch.int32, (n_seqs + 1,), "row_off")
-    return n_seqs, max_pages
+    n, m = block_table.shape
+    first = cache.k_codes
+    return n, m, _like(row_off, first, torch.int32, (n + 1,), "row_off"), _like(block_table, first, torch.int32, (n, m),
+                                                                                "block_table")
 
 
 def kv_cache_write(cache, k, v, row_off, kv_len, block_table):
     """Quantize k, v [rows, n_heads, D] into the cache's pages (quads_kv_cache_write)."""
-    rows, heads, dim, ld_k = _heads_view(k, "k")
-    rows_v, heads_v, dim_v, ld_v = _heads_view(v, "v")
-    if (heads, dim) != (cache.n_heads, cache.head_dim) or (rows_v, heads_v, dim_v) != (rows, heads, dim):
+    stream = _stream(cache.k_codes, "the cache")
+    rows, heads, dim, ld_k = _heads_view(k, cache.k_codes, "k")
+    rows_v, heads_v, dim_v, ld_v = _heads_view(v, cache.k_codes, "v")
+    if heads != cache.n_heads or dim != cache.head_dim or rows_v != rows or heads_v != heads or dim_v != dim:
         raise ValueError(f"k and v must be [rows, {cache.n_heads}, {cache.head_dim}], got {tuple(k.shape)} and "
                          f"{tuple(v.shape)}")
-    n_seqs, max_pages = _tables(cache, row_off, block_table)
-    _ints(kv_len, torch.int32, (n_seqs,), "kv_len")
-    _check(load().quads_kv_cache_write(cache.ref, _p(k), _p(v), rows, ld_k, ld_v, _p(row_off), _p(kv_len),
-                                       _p(block_table), n_seqs, max_pages, _s()), "quads_kv_cache_write")
+    n, m, off, table = _tables(cache, row_off, block_table)
+    kv = _like(kv_len, cache.k_codes, torch.int32, (n,), "kv_len")
+    _check(load().quads_kv_cache_write(cache.ref, k.data_ptr(), v.data_ptr(), rows, ld_k, ld_v, off, kv, table, n, m,
+                                       stream), "quads_kv_cache_write")
 
 
 def kv_cache_read(cache, row_off, block_table, rows, start=None, out_dtype=OUT_BF16, k_out=None, v_out=None):
     """Cached keys and values [rows, n_heads, D] of each sequence from position
     start[b] (0) on (quads_kv_cache_read); given outputs are written in place."""
-    n_seqs, max_pages = _tables(cache, row_off, block_table)
-    if start is not None:
-        _ints(start, torch.int32, (n_seqs,), "start")
+    first = cache.k_codes
+    stream = _stream(first, "the cache")
+    n, m, off, table = _tables(cache, row_off, block_table)
+    st = None if start is None else _like(start, first, torch.int32, (n,), "start")
     if out_dtype not in (OUT_BF16, OUT_F32):
         raise ValueError(f"unknown output dtype {out_dtype}")
     dt = torch.bfloat16 if out_dtype == OUT_BF16 else torch.float32
     shape = (rows, cache.n_heads, cache.head_dim)
-    out = []
-    for t, name in ((k_out, "k_out"), (v_out, "v_out")):
-        if t is None:
-            t = _empty(shape, dt, cache.k_codes.device)
-        else:
-            _ints(t, dt, shape, name)
-        out.append(t)
-    _check(load().quads_kv_cache_read(cache.ref, _p(row_off), _p(start), _p(block_table), n_seqs, max_pages, rows,
-                                      _p(out[0]), _p(out[1]), out_dtype, _s()), "quads_kv_cache_read")
-    return out[0], out[1]
+    if k_out is None:
+        k_out = first.new_empty(shape, dtype=dt)
+    if v_out is None:
+        v_out = first.new_empty(shape, dtype=dt)
+    _check(load().quads_kv_cache_read(cache.ref, off, st, table, n, m, rows, _like(k_out, first, dt, shape, "k_out"),
+                                      _like(v_out, first, dt, shape, "v_out"), out_dtype, stream),
+           "quads_kv_cache_read")
+    return k_out, v_out
 
 
 def _rope(q, k, positions, freq, interleaved, mscale, inverse, q_out, k_out):
-    rows, hq, dim, ld_q = _heads_view(q, "q")
-    hk, ld_k, ld_ko = 0, 0, 0
+    stream = _stream(q, "q")
+    rows, hq, dim, ld_q = _heads_view(q, q, "q")
+    hk = ld_k = ld_ko = 0
+    pk = pko = None
     if k is not None:
-        rows_k, hk, dim_k, ld_k = _heads_view(k, "k")
-        if (rows_k, dim_k) != (rows, dim):
+        rows_k, hk, dim_k, ld_k = _heads_view(k, q, "k")
+        if rows_k != rows or dim_k != dim:
             raise ValueError(f"q and k must have the same rows and head size, got {tuple(q.shape)} and {tuple(k.shape)}")
-        k_out = _empty((rows, hk, dim), torch.bfloat16, k.device) if k_out is None else k_out
-        if k_out.shape != k.shape:
-            raise ValueError("k_out must have k's shape")
-        ld_ko = _heads_view(k_out, "k_out")[3]
-    q_out = _empty((rows, hq, dim), torch.bfloat16, q.device) if q_out is None else q_out
-    if q_out.shape != q.shape:
-        raise ValueError("q_out must have q's shape")
-    ld_qo = _heads_view(q_out, "q_out")[3]
-    _ints(positions, torch.int64, (rows,), "positions")
-    _ints(freq, torch.float64, (freq.numel(),), "freq")
-    _check(load().quads_rope(_p(q), ld_q, hq, _p(k), ld_k, hk, rows, dim, _p(positions), _p(freq), 2 * freq.numel(),
-                             1 if interleaved else 0, float(mscale), 1 if inverse else 0, _p(q_out), ld_qo,
-                             _p(k_out), ld_ko, _s()), "quads_rope")
+        if k_out is None:
+            k_out, ld_ko = k.new_empty((rows, hk, dim)), hk * dim
+        else:
+            if k_out.shape != k.shape:
+                raise ValueError("k_out must have k's shape")
+            ld_ko = _heads_view(k_out, q, "k_out")[3]
+        pk, pko = k.data_ptr(), k_out.data_ptr()
+    if q_out is None:
+        q_out, ld_qo = q.new_empty((rows, hq, dim)), hq * dim
+    else:
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must have q's shape")
+        ld_qo = _heads_view(q_out, q, "q_out")[3]
+    n = freq.numel()
+    _check(load().quads_rope(q.data_ptr(), ld_q, hq, pk, ld_k, hk, rows, dim,
+                             _like(positions, q, torch.int64, (rows,), "positions"),
+                             _like(freq, q, torch.float64, (n,), "freq"), 2 * n, 1 if interleaved else 0, mscale,
+                             1 if inverse else 0, q_out.data_ptr(), ld_qo, pko, ld_ko, stream), "quads_rope")
     return q_out, k_out
 
 
@@ -809,22 +826,27 @@ def attention_paged(q, cache, row_off, kv_len, block_table, max_q_len, scale=Non
     """Attention of the new tokens' q [rows, heads_q, D] over the paged cache
     (quads_attention_paged): out [rows, heads_q, D]; lse [rows, heads_q] is
     filled when given.  scale None: D ** -0.5."""
-    rows, hq, dim, ld_q = _heads_view(q, "q")
+    first = cache.k_codes
+    stream = _stream(first, "the cache")
+    rows, hq, dim, ld_q = _heads_view(q, first, "q")
     if dim != cache.head_dim or hq % cache.n_heads:
         raise ValueError(f"q must be [rows, a multiple of {cache.n_heads}, {cache.head_dim}], got {tuple(q.shape)}")
-    n_seqs, max_pages = _tables(cache, row_off, block_table)
-    _ints(kv_len, torch.int32, (n_seqs,), "kv_len")
+    n, m, off, table = _tables(cache, row_off, block_table)
+    kv = _like(kv_len, first, torch.int32, (n,), "kv_len")
     if out is None:
-        out = _empty((rows, hq, dim), torch.bfloat16, q.device)
+        out = q.new_empty((rows, hq, dim))
+        po = out.data_ptr()
     else:
-        _ints(out, torch.bfloat16, (rows, hq, dim), "out")
-    if lse is not None:
-        _ints(lse, torch.float32, (rows, hq), "lse")
+        po = _like(out, first, torch.bfloat16, (rows, hq, dim), "out")
+    pl = None if lse is None else _like(lse, first, torch.float32, (rows, hq), "lse")
+    lib = load()
     if ws is None:
-        n = attention_paged_workspace_bytes(cache, rows, hq, n_seqs, max_pages, max_q_len)
-        ws = _empty((n,), torch.uint8, q.device) if n else None
-    _check(load().quads_attention_paged(
-        _p(q), rows, ld_q, hq, cache.ref, _p(row_off), _p(kv_len), _p(block_table), n_seqs, max_pages, int(max_q_len),
-        dim ** -0.5 if scale is None else float(scale), int(window), _p(out), _p(lse), _p(ws),
-        0 if ws is None else ws.numel() * ws.element_size(), _s()), "quads_attention_paged")
+        need = lib.quads_attention_paged_workspace_bytes(cache.ref, rows, hq, n, m, max_q_len)
+        ws = first.new_empty((need,)) if need else None
+    elif ws.get_device() != first.get_device() or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous tensor on {first.device}")
+    pw, nw = (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
+    _check(lib.quads_attention_paged(q.data_ptr(), rows, ld_q, hq, cache.ref, off, kv, table, n, m, max_q_len,
+                                     dim ** -0.5 if scale is None else scale, window, po, pl, pw, nw, stream),
+           "quads_attention_paged")
     return out

@@ -64,18 +64,24 @@ __global__ void __launch_bounds__(128) attention_kernel(AttnArgs p) {
 }
 
 // CTAs of the kernel for few rows: as many as are resident at once.
-int dec_grid(int nt) { return (nt == 1 ? 4 : 3) * num_sms(); }
+int dec_grid(int nt) {
+  const int n = dec_ctas_per_sm(nt) * num_sms();
+  return n < kMaxRuns ? n : kMaxRuns;
+}
 constexpr int kDecMinQuota = 4;      // tiles of a run: shorter ones cost more in joining than they save
 
 size_t dec_workspace(int D, int nt) {
-  return static_cast<size_t>(2) * dec_grid(nt) * (8 * nt) * (D * sizeof(float) + sizeof(float2));
+  return static_cast<size_t>(dec_grid(nt)) * (2 * (8 * nt) * (D * sizeof(float) + sizeof(float2)) + sizeof(int4));
 }
 
 template <int D, int NT>
 int launch_decode(AttnArgs p, void* ws, int unit_rows, cudaStream_t stream) {
   const int grid = dec_grid(NT);
-  p.part_o = static_cast<float*>(ws);
+  const int64_t units = static_cast<int64_t>(p.c.n_seqs) * p.c.n_heads;
+  p.cuts = static_cast<int4*>(ws);
+  p.part_o = reinterpret_cast<float*>(p.cuts + grid);
   p.part_ml = reinterpret_cast<float2*>(p.part_o + static_cast<size_t>(2) * grid * (8 * NT) * D);
+  p.by_unit = units <= grid;
   attention_decode_kernel<D, NT><<<grid, kDecThreads, 0, stream>>>(p, kDecMinQuota);
   QUADS_TRY(check_launch("attention_decode_kernel"));
   // the joining kernel is resident before the last run ends and waits for it
@@ -84,12 +90,12 @@ int launch_decode(AttnArgs p, void* ws, int unit_rows, cudaStream_t stream) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
   // rows on blocks of their own where few units are cut into many runs
-  cfg.gridDim = dim3(grid - 1, static_cast<int64_t>(p.c.n_seqs) * p.c.n_heads * 8 <= grid ? unit_rows : 1);
-  cfg.blockDim = dim3(4 * D);
+  cfg.gridDim = dim3(static_cast<unsigned>(p.by_unit ? units : grid), units * 8 <= grid ? unit_rows : 1);
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, attention_combine_kernel<D, NT>, p, grid, kDecMinQuota) != cudaSuccess)
+  if (cudaLaunchKernelEx(&cfg, attention_combine_kernel<D, NT>, p) != cudaSuccess)
     return check_launch("attention_combine_kernel");
   count_launches(2);
   return QUADS_OK;
@@ -119,6 +125,8 @@ int quads_attention_paged(const uint16_t* q, int64_t rows, int64_t ld_q, int hea
   QUADS_TRY(check_cache(cache));
   QUADS_TRY(check_seqs(row_off, block_table, n_seqs, max_pages));
   QUADS_REQUIRE(rows >= 0 && rows < (int64_t(1) << 30), QUADS_ERR_INVALID_ARG, "rows must be in [0, 2^30)");
+  QUADS_REQUIRE(rows * cache->n_heads < (int64_t(1) << 31), QUADS_ERR_UNSUPPORTED_SHAPE,
+                "rows * n_heads must be below 2^31");
   QUADS_REQUIRE(heads_q >= 1 && heads_q <= 4096 && heads_q % cache->n_heads == 0, QUADS_ERR_UNSUPPORTED_SHAPE,
                 "heads_q (%d) must be a multiple of the cache's %d heads, at most 4096", heads_q, cache->n_heads);
   QUADS_REQUIRE(ld_q >= static_cast<int64_t>(heads_q) * cache->head_dim && ld_q % 8 == 0, QUADS_ERR_INVALID_ARG,
@@ -139,6 +147,9 @@ int quads_attention_paged(const uint16_t* q, int64_t rows, int64_t ld_q, int hea
   p.group_div = make_fastdiv(static_cast<uint32_t>(p.group));
   const int64_t unit_rows = static_cast<int64_t>(max_q_len) * p.group;
   if (unit_rows <= 16) {
+    const int64_t tiles = static_cast<int64_t>(max_pages) * cache->page_size / kDecTile + 2;
+    QUADS_REQUIRE(tiles < (int64_t(1) << 30) && tiles * n_seqs * cache->n_heads < (int64_t(1) << 30),
+                  QUADS_ERR_UNSUPPORTED_SHAPE, "n_seqs * n_heads * max_pages * page_size must be below 2^36");
     const int n = static_cast<int>(unit_rows);
     if (cache->head_dim == 64)
       return n <= 8 ? launch_decode<64, 1>(p, ws, n, stream) : launch_decode<64, 2>(p, ws, n, stream);

@@ -22,6 +22,11 @@ struct AttnArgs {
   // unnormalised sums, and {maximum, sum} of each row
   float* part_o;
   float2* part_ml;
+  // {slot of the first part or -1, CTA of the last, first row * n_heads + head,
+  // rows} of each unit (by_unit), or of the one that each CTA begins and does
+  // not end
+  int4* cuts;
+  int by_unit;
 };
 
 // A sequence of a call: its rows, and the keys that they can see.
@@ -41,7 +46,7 @@ __device__ __forceinline__ SeqInfo seq_info(const AttnArgs& p, int b) {
   s.nq = min(n, p.max_q);
   const int64_t pos0 = static_cast<int64_t>(max(__ldg(p.kv_len + b), 0)) - n;      // > -2^30: rows < 2^30
   s.pos0 = static_cast<int>(pos0);
-  const int64_t cap = static_cast<int64_t>(p.c.max_pages) * p.c.page_size;
+  const int64_t cap = p.c.n_pages > 0 ? static_cast<int64_t>(p.c.max_pages) * p.c.page_size : 0;
   s.hi = static_cast<int>(max(int64_t(0), min(cap, pos0 + s.nq)));
   int64_t lo = p.window > 0 ? pos0 - p.window + 1 : 0;
   lo = min(max(lo, int64_t(0)), static_cast<int64_t>(s.hi));
@@ -78,13 +83,14 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // An E4M3 scale as {v, v} FP16 with v = val(s) * 2^-8: the code shifted into
-// FP16's exponent and mantissa (bias 15 instead of 7; subnormals alike).  No
-// code gives a NaN or an infinity (0x7F gives 480 * 2^-8), so bytes of places
-// that nothing was written to cannot pass through a weight of zero.
-__device__ __forceinline__ uint32_t scale_f16x2(uint32_t s) { return (s & 0x7Fu) * 0x00800080u; }
-// Two such scales.
+// FP16's exponent and mantissa (bias 15 instead of 7; subnormals alike).
+__device__ __forceinline__ uint32_t scale_f16x2(uint32_t s) { return s * 0x00800080u; }
+// Two such scales, without their sign bits: no code then gives a NaN or an
+// infinity (0x7F gives 480 * 2^-8), so that bytes of places that nothing was
+// written to cannot pass through a weight of zero.  (A score that is NaN is
+// replaced where it is masked, so the keys' scales need no such care.)
 __device__ __forceinline__ uint32_t scale_pair_f16x2(uint32_t s0, uint32_t s1) {
-  return ((s0 & 0x7Fu) << 7) | ((s1 & 0x7Fu) << 23);
+  return ((s0 + (s1 << 16)) & 0x007F007Fu) << 7;
 }
 constexpr float kScaleUnit = 256.0f;      // what the 2^-8 above is undone with
 

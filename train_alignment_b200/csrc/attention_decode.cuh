@@ -28,71 +28,87 @@ namespace quads {
 constexpr int kDecThreads = 128;
 constexpr int kDecWarps = kDecThreads / 32;
 constexpr int kDecTile = 16 * kDecWarps;
+// resident CTAs of an SM: its registers hold 96 (160) a thread
+__host__ __device__ constexpr int dec_ctas_per_sm(int nt) { return nt == 1 ? 4 : 3; }
+constexpr int kMaxRuns = 1024;      // CTAs of a launch
 
 __device__ __forceinline__ int dec_tiles(const SeqInfo& s) {
   if (s.nq <= 0) return 0;
   return max(1, (s.hi - s.lo + kDecTile - 1) / kDecTile);
 }
 
-// Tiles of all units, and the sequence that holds tile w, found by a block of
-// kN threads (every thread gets the answer).
-template <int kN>
+// The run of this CTA: tiles [w0, w1) of all units' (fewer than 2^30, checked
+// on the host), and the sequence of the first with the first tile of its first
+// unit.  Calls of up to kDecThreads sequences scan them once and keep them.
 struct DecPlan {
-  int warp_s[kN / 32];
-  int b;
-  long long base;      // first tile of the sequence's first unit
-  long long sum;
+  int warp_s[kDecWarps];
+  int b, base;
+  SeqInfo seq[kDecThreads];
 
-  __device__ __forceinline__ long long total(const AttnArgs& p) {
-    const int lane = threadIdx.x & 31;
-    long long n = 0;
-    for (int i = threadIdx.x; i < p.c.n_seqs; i += kN) n += dec_tiles(seq_info(p, i));
-#pragma unroll
-    for (int d = 16; d; d >>= 1) n += __shfl_xor_sync(0xffffffffu, n, d);
-    if (threadIdx.x == 0) sum = 0;
-    __syncthreads();
-    if (lane == 0 && n) atomicAdd(reinterpret_cast<unsigned long long*>(&sum), static_cast<unsigned long long>(n));
-    __syncthreads();
-    return sum * p.c.n_heads;
-  }
-  // w < total()
-  __device__ __forceinline__ void find(const AttnArgs& p, long long w) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    long long run = 0;                                   // tiles (per head) before this chunk
-    for (int c0 = 0; c0 < p.c.n_seqs; c0 += kN) {
-      const int i = c0 + threadIdx.x;
-      const int n = i < p.c.n_seqs ? dec_tiles(seq_info(p, i)) : 0;
-      int incl = n;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, incl, d);
-        if (lane >= d) incl += v;
-      }
-      if (lane == 31) warp_s[warp] = incl;
-      __syncthreads();
-      long long before = run;
-      int all = 0;
-#pragma unroll
-      for (int k = 0; k < kN / 32; ++k) {
-        if (k < warp) before += warp_s[k];
-        all += warp_s[k];
-      }
-      const long long first = (before + incl - n) * p.c.n_heads, last = (before + incl) * p.c.n_heads;
-      if (n > 0 && w >= first && w < last) {
-        b = i;
-        base = first;
-      }
-      run += all;
-      __syncthreads();
-      if (w < run * p.c.n_heads) return;                 // the same for every thread
+  // tiles (of one head) of sequences c0 .. c0 + kDecThreads - 1: this
+  // thread's, those before it, and all
+  __device__ __forceinline__ int scan(const AttnArgs& p, int c0, int& before, int& n) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, i = c0 + threadIdx.x;
+    n = 0;
+    if (i < p.c.n_seqs) {
+      const SeqInfo s = seq_info(p, i);
+      n = dec_tiles(s);
+      seq[threadIdx.x] = s;
+      if (n == 0 && p.by_unit && blockIdx.x == 0)
+        for (int h = 0; h < p.c.n_heads; ++h) p.cuts[i * p.c.n_heads + h] = make_int4(-1, 0, 0, 0);
     }
+    int incl = n;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += v;
+    }
+    if (lane == 31) warp_s[warp] = incl;
+    __syncthreads();
+    before = incl - n;
+    int all = 0;
+#pragma unroll
+    for (int k = 0; k < kDecWarps; ++k) {
+      if (k < warp) before += warp_s[k];
+      all += warp_s[k];
+    }
+    return all;
+  }
+
+  // false: nothing to do
+  __device__ __forceinline__ bool run(const AttnArgs& p, int min_quota, int& quota, int& w0, int& w1) {
+    int before, n, all = 0;
+    for (int c0 = 0; c0 < p.c.n_seqs; c0 += kDecThreads) {
+      if (c0) __syncthreads();
+      all += scan(p, c0, before, n);
+    }
+    const int total = all * p.c.n_heads;
+    quota = max(static_cast<int>(static_cast<unsigned>(total + gridDim.x - 1) / gridDim.x), min_quota);
+    const int64_t first = static_cast<int64_t>(quota) * blockIdx.x;
+    if (first >= total) return false;
+    w0 = static_cast<int>(first);
+    w1 = min(total, w0 + quota);
+    int run = 0;
+    for (int c0 = 0;; c0 += kDecThreads) {
+      if (p.c.n_seqs > kDecThreads) {
+        __syncthreads();
+        const int t = scan(p, c0, before, n);
+        before += run;
+        run += t;
+      }
+      if (n > 0 && w0 >= before * p.c.n_heads && w0 < (before + n) * p.c.n_heads) {
+        b = c0 + threadIdx.x;
+        base = before * p.c.n_heads;
+      }
+      if (p.c.n_seqs <= kDecThreads || w0 < run * p.c.n_heads) break;      // the same for every thread
+    }
+    __syncthreads();
+    return true;
+  }
+  __device__ __forceinline__ SeqInfo info(const AttnArgs& p, int i) const {
+    return p.c.n_seqs <= kDecThreads ? seq[i] : seq_info(p, i);
   }
 };
-
-__device__ __forceinline__ long long dec_quota(long long total, int n_cta, int min_quota) {
-  const long long q = (total + n_cta - 1) / n_cta;
-  return q > min_quota ? q : min_quota;
-}
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -107,74 +123,131 @@ __device__ __forceinline__ uint32_t move_trans(uint32_t x) {
   return y;
 }
 
-// A lane's part of 16 keys and values as they lie in the cache.
+// A warp's ring of steps in shared memory: 16 keys' and values' codes and
+// scales as they lie in the cache, copied 16 bytes at a time.  Chunk c of a
+// value's codes is at c ^ (key / 2 % 4) (D = 128), and key i of a matrix of
+// eight is row i ^ (i / 2 % 2) of the step: both matrix operands are then read
+// without bank conflicts.
+constexpr int kDecStages = 4;
+static_assert(kDecStages == 4, "the look-up's turns (16 and 32 steps) are met at u == 1");
+__host__ __device__ constexpr int dec_stage_bytes(int D) { return 16 * (D + D / 8); }
+__device__ __forceinline__ int dec_key(int i) { return i ^ ((i >> 1) & 1); }
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+
+// Where a lane copies its chunks from (for row 0 of the cache) and to (for a
+// step's place at 0).
+template <int D>
+struct DecCopy {
+  static constexpr int kChunks = D / 32;                 // 16-byte chunks of a key's codes
+  static constexpr int kScales = D / 16;                 // and of 16 keys' scales
+  const uint8_t *k, *v, *s;
+  uint32_t dst_v, dst_s;                                 // keys' codes: 16 * lane (+ 512)
+
+  __device__ __forceinline__ DecCopy(const CacheArgs& c, int lane) {
+    const int key = lane / kChunks, ch = lane % kChunks;
+    const int sw = D == 128 ? ch ^ ((key >> 1) & 3) : ch;
+    k = c.k_codes + 16 * lane;
+    v = c.v_codes + 16 * lane;
+    s = (lane < kScales ? c.k_scales : c.v_scales) + 16 * (lane % kScales);
+    dst_v = 8 * D + key * (D / 2) + 16 * sw;
+    dst_s = 16 * D + 16 * lane;
+  }
+  __device__ __forceinline__ void load(uint32_t row, uint32_t dst, int lane) const {
+    const uint64_t at = static_cast<uint64_t>(row) * (D / 2);
+#pragma unroll
+    for (int i = 0; i < kChunks / 2; ++i) {              // key + 8: the same swizzle
+      cp_async16(dst + 512 * i + 16 * lane, k + at + 512 * i);
+      cp_async16(dst + 512 * i + dst_v, v + at + 512 * i);
+    }
+    if (lane < 2 * kScales) cp_async16(dst + dst_s, s + static_cast<uint64_t>(row) * (D / 16));
+  }
+};
+
+// A lane's part of a step: keys g and g + 8, elements [t D / 4, (t + 1) D / 4);
+// values 2t, 2t + 1, 2t + 8, 2t + 9, elements [g D / 8, (g + 1) D / 8).
 template <int D>
 struct DecRaw {
-  uint32_t k[2][D / 32];       // keys g, g + 8: 8 codes a word
+  uint32_t k[2][D / 32];       // 8 codes a word
   uint32_t ks[2];              // their scales: D / 64 bytes
-  uint32_t v[4][D / 64];       // values 2t, 2t + 1, 2t + 8, 2t + 9
+  uint32_t v[4][D / 64];
   uint32_t vs[4];
 
-  __device__ __forceinline__ void load(const CacheArgs& c, int64_t row, int g, int t) {
+  __device__ __forceinline__ void read(const uint8_t* st, int g, int t) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int64_t r = row + g + 8 * i;
+      const int key = dec_key(g) + 8 * i;
       if constexpr (D == 128) {
-        const uint4 x = __ldg(reinterpret_cast<const uint4*>(c.k_codes + r * 64) + t);
+        const uint4 x = *reinterpret_cast<const uint4*>(st + key * 64 + t * 16);
         k[i][0] = x.x; k[i][1] = x.y; k[i][2] = x.z; k[i][3] = x.w;
-        ks[i] = __ldg(reinterpret_cast<const uint16_t*>(c.k_scales + r * 8) + t);
+        ks[i] = *reinterpret_cast<const uint16_t*>(st + 16 * D + key * 8 + t * 2);
       } else {
-        const uint2 x = __ldg(reinterpret_cast<const uint2*>(c.k_codes + r * 32) + t);
+        const uint2 x = *reinterpret_cast<const uint2*>(st + key * 32 + t * 8);
         k[i][0] = x.x; k[i][1] = x.y;
-        ks[i] = __ldg(c.k_scales + r * 4 + t);
+        ks[i] = st[16 * D + key * 4 + t];
       }
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int64_t r = row + 2 * t + (i & 1) + 8 * (i >> 1);
+      const int key = dec_key(2 * t + (i & 1)) + 8 * (i >> 1);
+      const uint8_t* const vp = st + 8 * D + key * (D / 2);
       if constexpr (D == 128) {
-        const uint2 x = __ldg(reinterpret_cast<const uint2*>(c.v_codes + r * 64) + g);
+        const uint2 x = *reinterpret_cast<const uint2*>(vp + (((g >> 1) ^ ((key >> 1) & 3)) * 16) + (g & 1) * 8);
         v[i][0] = x.x; v[i][1] = x.y;
-        vs[i] = __ldg(c.v_scales + r * 8 + g);
+        vs[i] = st[16 * D + 128 + key * 8 + g];
       } else {
-        v[i][0] = __ldg(reinterpret_cast<const uint32_t*>(c.v_codes + r * 32) + g);
-        vs[i] = __ldg(c.v_scales + r * 4 + (g >> 1));
+        v[i][0] = *reinterpret_cast<const uint32_t*>(vp + g * 4);
+        vs[i] = st[16 * D + 64 + key * 4 + (g >> 1)];
       }
     }
   }
 };
 
+constexpr uint32_t kNoRow = 0xFFFFFFFFu;     // in place of a cache row: no page
+constexpr float kNoMax = -1e30f;             // the running maximum before the first key: finite, so that
+                                             // differences of maxima are never NaN
+
 template <int D, int NT>
-__global__ void __launch_bounds__(kDecThreads, NT == 1 ? 4 : 3) attention_decode_kernel(AttnArgs p, int min_quota) {
+__global__ void __launch_bounds__(kDecThreads, dec_ctas_per_sm(NT)) attention_decode_kernel(AttnArgs p, int min_quota) {
   constexpr int kRows = 8 * NT;
   constexpr int kMT = D / 16;                           // 16-element tiles of O^T
-  __shared__ float o_s[kDecWarps][kRows][D];
+  constexpr int kStage = dec_stage_bytes(D), kRing = kDecWarps * kDecStages * kStage;
+  constexpr int kJoin = kDecWarps * kRows * D * 4;
+  __shared__ __align__(128) uint8_t buf_s[kRing > kJoin ? kRing : kJoin];    // the warps' rings, then their sums
+  float (*const o_s)[kRows][D] = reinterpret_cast<float (*)[kRows][D]>(buf_s);
   __shared__ float2 ml_s[kDecWarps][kRows];
   __shared__ float f_s[kDecWarps][kRows];               // weight of each warp's sums; then 1 / l in [0]
-  __shared__ DecPlan<kDecThreads> plan;
+  __shared__ DecPlan plan;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
-  const long long total = plan.total(p);
-  const long long quota = dec_quota(total, gridDim.x, min_quota);
-  const long long w0 = quota * blockIdx.x, w1 = min(total, w0 + quota);
-  if (w0 >= total) return;
-  plan.find(p, w0);
-  int b = plan.b;
-  long long base = plan.base;
+  int quota, w0, w1;
+  bool told = false;                                    // thread 0: this run's cut is written
+  if (!plan.run(p, min_quota, quota, w0, w1)) {
+    if (!p.by_unit && threadIdx.x == 0) p.cuts[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    return;
+  }
+  int b = plan.b, base = plan.base;
 
-  for (long long w = w0; w < w1;) {
-    SeqInfo s = seq_info(p, b);
+  for (int w = w0; w < w1;) {
+    SeqInfo s = plan.info(p, b);
     int nt = dec_tiles(s);
-    while (w >= base + static_cast<long long>(nt) * p.c.n_heads) {      // on to the next sequence with rows
-      base += static_cast<long long>(nt) * p.c.n_heads;
-      s = seq_info(p, ++b);
+    while (w >= base + nt * p.c.n_heads) {              // on to the next sequence with rows
+      base += nt * p.c.n_heads;
+      s = plan.info(p, ++b);
       nt = dec_tiles(s);
     }
-    const int head = static_cast<int>((w - base) / nt);
-    const int tile0 = static_cast<int>(w - base - static_cast<long long>(head) * nt);
-    const int tile1 = static_cast<int>(min(static_cast<long long>(nt), tile0 + (w1 - w)));
+    const int head = static_cast<int>(static_cast<unsigned>(w - base) / static_cast<unsigned>(nt));
+    const int tile0 = w - base - head * nt;
+    const int tile1 = min(nt, tile0 + (w1 - w));
     const int R = min(s.nq * p.group, kRows);
 
     // queries: lane (g, t) holds elements [t D / 4, (t + 1) D / 4) of row g of each group of 8
@@ -213,45 +286,34 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 4 : 3) attention_decode
         c2[n][1] = __shfl_sync(0xffffffffu, f, 8 * t + 4);
       }
     }
-    int pos[NT][2];                                     // positions of rows 2t, 2t + 1
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) pos[n][i] = s.pos0 + static_cast<int>(fast_div(8 * n + 2 * t + i, p.group_div));
-
-    float o[NT][kMT][4], m[NT][2], l[NT][2];
+    // up: kShift minus a row's running maximum, so that one FMA gives the
+    // exponent of a weight
+    float o[NT][kMT][4], up[NT][2], l[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
       for (int i = 0; i < kMT; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.0f;
-      m[n][0] = m[n][1] = -CUDART_INF_F;
+      up[n][0] = up[n][1] = kShift - kNoMax;
       l[n][0] = l[n][1] = 0.0f;
     }
 
-    // the warp's steps of 16 keys, one per tile; a step's keys share a page
+    // The warp's steps of 16 keys, one per tile.  A step's keys share a page:
+    // lane i looks up the cache row of step i of 32, the next 32 half way
+    // through these.  A step without a page reads row 0 and masks it.
     const int pos_last = s.pos0 + s.nq - 1;
-    auto key0 = [&](int tile) { return s.lo + tile * kDecTile + 16 * warp; };
-    auto row_of = [&](int j, int64_t& row) {            // cache row of key j, false without a page
-      if (j >= s.hi) return false;
+    const int j_first = s.lo + tile0 * kDecTile + 16 * warp;
+    const int steps = min(tile1 - tile0, (s.hi - j_first + kDecTile - 1) / kDecTile);     // those with a key below hi
+    auto lookup = [&](int step) -> uint32_t {
+      if (step >= steps) return 0u;
       int at;
-      const int page = page_of(p.c, b, j, at);
-      row = page >= 0 ? cache_row(p.c, page, head, at) : 0;
-      return page >= 0;
+      const int page = page_of(p.c, b, j_first + step * kDecTile, at);
+      return page >= 0 ? static_cast<uint32_t>(cache_row(p.c, page, head, at)) : kNoRow;
     };
-    DecRaw<D> cur, nxt;
-    int64_t row = 0, row2 = 0;
-    bool have = row_of(key0(tile0), row);
-    if (have) nxt.load(p.c, row, g, t);
-    bool have2 = tile0 + 1 < tile1 && row_of(key0(tile0 + 1), row2);
-    for (int tile = tile0; tile < tile1; ++tile) {
-      const bool now = have;
-      cur = nxt;
-      have = have2;
-      if (have) nxt.load(p.c, row2, g, t);
-      have2 = tile + 2 < tile1 && row_of(key0(tile + 2), row2);
-      if (!now) continue;
-      const int j0 = key0(tile);
+    uint32_t rows_now = lookup(lane), rows_next = 0u;
+    uint32_t gone_now = __ballot_sync(0xffffffffu, rows_now == kNoRow), gone_next = 0u;   // bit i: step i has no page
+    if (rows_now == kNoRow) rows_now = 0u;
 
+    auto attend = [&](const DecRaw<D>& x, int j0, bool gone) {
       // S^T = K Q^T
       float sc[NT][4];
 #pragma unroll
@@ -259,10 +321,10 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 4 : 3) attention_decode
 #pragma unroll
       for (int j = 0; j < D / 32; ++j) {
         uint32_t a[4], bb[4];
-        e2m1x8_to_f16x2(cur.k[0][j], a);
-        e2m1x8_to_f16x2(cur.k[1][j], bb);
+        e2m1x8_to_f16x2(x.k[0][j], a);
+        e2m1x8_to_f16x2(x.k[1][j], bb);
         const int sh = D == 128 ? 8 * (j >> 1) : 0;
-        const uint32_t s0 = scale_f16x2(cur.ks[0] >> sh), s1 = scale_f16x2(cur.ks[1] >> sh);
+        const uint32_t s0 = scale_f16x2(sh ? x.ks[0] >> 8 : x.ks[0] & 0xFFu), s1 = scale_f16x2(sh ? x.ks[1] >> 8 : x.ks[1] & 0xFFu);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           a[i] = hmul2_rn(a[i], s0);
@@ -274,68 +336,73 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 4 : 3) attention_decode
           mma_f16(sc[n], a[2], bb[2], a[3], bb[3], qf[n][4 * j + 2], qf[n][4 * j + 3]);
         }
       }
-      // scores in powers of two; masked where a row does not see the key
+      // exponents of the weights; -inf where a row does not see the key
+      float y[NT][4], top = -CUDART_INF_F;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sc[n][i] *= c2[n][i & 1];
-      if (j0 + 15 > s.pos0 || j0 + 16 > s.hi || (p.window > 0 && j0 <= pos_last - p.window)) {
+        for (int i = 0; i < 4; ++i) y[n][i] = __fmaf_rn(sc[n][i], c2[n][i & 1], up[n][i & 1]);
+      if (gone || j0 + 15 > s.pos0 || j0 + 16 > s.hi || (p.window > 0 && j0 <= pos_last - p.window)) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int j = j0 + g + 8 * (i >> 1);
-            const bool see = j <= pos[n][i & 1] && j < s.hi && (p.window <= 0 || j > pos[n][i & 1] - p.window);
-            if (!see) sc[n][i] = -CUDART_INF_F;
+            const int j = j0 + dec_key(g) + 8 * (i >> 1);
+            const int pos = s.pos0 + static_cast<int>(fast_div(8 * n + 2 * t + (i & 1), p.group_div));
+            const bool see = !gone && j <= pos && j < s.hi && (p.window <= 0 || j > pos - p.window);
+            if (!see) y[n][i] = -CUDART_INF_F;
           }
       }
-      bool over = false;
+      // the sums are rescaled only when a score is kLag above its row's
+      // maximum so far
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) over |= sc[n][i] > m[n][i & 1] + kLag;
-      if (__any_sync(0xffffffffu, over)) {
+        for (int i = 0; i < 4; ++i) top = fmaxf(top, y[n][i]);
+      if (__any_sync(0xffffffffu, top > kShift + kLag)) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            float x = fmaxf(sc[n][i], sc[n][i + 2]);
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-            const float mn = fmaxf(m[n][i], x);
-            const float a = m[n][i] == -CUDART_INF_F ? 0.0f : ex2(m[n][i] - mn);
-            m[n][i] = mn;
+            const float x0 = y[n][i] == -CUDART_INF_F ? -CUDART_INF_F : sc[n][i] * c2[n][i];
+            const float x1 = y[n][i + 2] == -CUDART_INF_F ? -CUDART_INF_F : sc[n][i + 2] * c2[n][i];
+            float z = fmaxf(x0, x1);
+            z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, 4));
+            z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, 8));
+            z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, 16));
+            const float un = fminf(up[n][i], kShift - z);
+            const float a = ex2(un - up[n][i]);
+            up[n][i] = un;
             l[n][i] *= a;
 #pragma unroll
             for (int d = 0; d < kMT; ++d) {
               o[n][d][i] *= a;
               o[n][d][i + 2] *= a;
             }
+            y[n][i] = x0 + un;
+            y[n][i + 2] = x1 + un;
           }
       }
       uint32_t pb[NT][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const float m0 = m[n][0] == -CUDART_INF_F ? 0.0f : m[n][0] - kShift;
-        const float m1 = m[n][1] == -CUDART_INF_F ? 0.0f : m[n][1] - kShift;
-        const float e0 = ex2(sc[n][0] - m0), e1 = ex2(sc[n][1] - m1), e2 = ex2(sc[n][2] - m0), e3 = ex2(sc[n][3] - m1);
+        const float e0 = ex2(y[n][0]), e1 = ex2(y[n][1]), e2 = ex2(y[n][2]), e3 = ex2(y[n][3]);
         l[n][0] += e0 + e2;
         l[n][1] += e1 + e3;
         pb[n][0] = move_trans(pack_f16x2(e0, e1));
         pb[n][1] = move_trans(pack_f16x2(e2, e3));
       }
       // O^T += V^T P^T
-      const uint32_t sa = scale_pair_f16x2(cur.vs[0], cur.vs[1]), sb = scale_pair_f16x2(cur.vs[2], cur.vs[3]);
+      const uint32_t sa = scale_pair_f16x2(x.vs[0], x.vs[1]), sb = scale_pair_f16x2(x.vs[2], x.vs[3]);
 #pragma unroll
       for (int j = 0; j < D / 64; ++j) {
         // bytes {value 2t, value 2t + 1} of elements 0, 2, 4, 6 and 1, 3, 5, 7 of the word
         constexpr uint32_t kLow = 0x0F0F0F0Fu;
         uint32_t a0[4], a1[4], b0[4], b1[4];
-        e2m1x8_to_f16x2((cur.v[0][j] & kLow) | ((cur.v[1][j] << 4) & ~kLow), a0);
-        e2m1x8_to_f16x2(((cur.v[0][j] >> 4) & kLow) | (cur.v[1][j] & ~kLow), a1);
-        e2m1x8_to_f16x2((cur.v[2][j] & kLow) | ((cur.v[3][j] << 4) & ~kLow), b0);
-        e2m1x8_to_f16x2(((cur.v[2][j] >> 4) & kLow) | (cur.v[3][j] & ~kLow), b1);
+        e2m1x8_to_f16x2((x.v[0][j] & kLow) | ((x.v[1][j] << 4) & ~kLow), a0);
+        e2m1x8_to_f16x2(((x.v[0][j] >> 4) & kLow) | (x.v[1][j] & ~kLow), a1);
+        e2m1x8_to_f16x2((x.v[2][j] & kLow) | ((x.v[3][j] << 4) & ~kLow), b0);
+        e2m1x8_to_f16x2(((x.v[2][j] >> 4) & kLow) | (x.v[3][j] & ~kLow), b1);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           a0[i] = hmul2_rn(a0[i], sa);
@@ -346,7 +413,49 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 4 : 3) attention_decode
           for (int n = 0; n < NT; ++n) mma_f16(o[n][4 * j + i], a0[i], a1[i], b0[i], b1[i], pb[n][0], pb[n][1]);
         }
       }
+    };
+
+    // one step being computed, kDecStages - 1 on their way
+    const uint8_t* const ring = buf_s + warp * (kDecStages * kStage);
+    const uint32_t ring_a = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
+    const DecCopy<D> copy(p.c, lane);
+#pragma unroll
+    for (int i = 0; i < kDecStages - 1; ++i) {
+      const uint32_t row = __shfl_sync(0xffffffffu, rows_now, i);
+      if (i < steps) copy.load(row, ring_a + i * kStage, lane);
+      cp_async_commit();
     }
+    uint32_t gone_cur = gone_now;
+    for (int step0 = 0; step0 < steps; step0 += kDecStages) {
+#pragma unroll
+      for (int u = 0; u < kDecStages; ++u) {             // step0 + u lies in place u of the ring
+        const int step = step0 + u;
+        if (step >= steps) break;
+        cp_async_wait<kDecStages - 2>();
+        __syncwarp();                                   // the step has landed, and its predecessor's place is free
+        const int ahead = step + kDecStages - 1;
+        if (u == 1) {                                   // ahead is a multiple of kDecStages
+          if ((ahead & 31) == 16) {
+            rows_next = lookup(ahead + 16 + lane);
+            gone_next = __ballot_sync(0xffffffffu, rows_next == kNoRow);
+            if (rows_next == kNoRow) rows_next = 0u;
+          }
+          if ((ahead & 31) == 0) {
+            rows_now = rows_next;
+            gone_now = gone_next;
+          }
+        }
+        const uint32_t row = __shfl_sync(0xffffffffu, rows_now, ahead & 31);
+        if (ahead < steps) copy.load(row, ring_a + (u + kDecStages - 1) % kDecStages * kStage, lane);
+        cp_async_commit();
+        if (u == 0 && (step & 31) == 0) gone_cur = gone_now;      // ahead has passed into this step's 32
+        DecRaw<D> x;
+        x.read(ring + u * kStage, g, t);
+        attend(x, j_first + step * kDecTile, (gone_cur >> (step & 31)) & 1u);
+      }
+    }
+    cp_async_wait<0>();
+    __syncthreads();
 
     // join the four warps: rows 2t, 2t + 1 of each group, elements [g D / 8, (g + 1) D / 8)
 #pragma unroll
@@ -358,23 +467,33 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 4 : 3) attention_decode
         x += __shfl_xor_sync(0xffffffffu, x, 8);
         x += __shfl_xor_sync(0xffffffffu, x, 16);
         const int r = 8 * n + 2 * t + i;
-        if (g == 0) ml_s[warp][r] = make_float2(m[n][i], x);
+        if (g == 0) ml_s[warp][r] = make_float2(kShift - up[n][i], x);
         float4* dst = reinterpret_cast<float4*>(&o_s[warp][r][g * (D / 8)]);
 #pragma unroll
         for (int d = 0; d < kMT / 2; ++d)
           dst[d] = make_float4(o[n][2 * d][i], o[n][2 * d][i + 2], o[n][2 * d + 1][i], o[n][2 * d + 1][i + 2]);
       }
     __syncthreads();
+    const int slot = 2 * blockIdx.x + (w == w0 ? 0 : 1);
     const bool whole = tile0 == 0 && tile1 == nt;
-    const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (w == w0 ? 0 : 1);
+    // the run that begins a unit says whether and where others go on with it
+    if (tile0 == 0 && threadIdx.x == 0) {
+      const int last = static_cast<int>(static_cast<unsigned>(w + nt - 1) / static_cast<unsigned>(quota));
+      const int4 cut = make_int4(whole ? -1 : slot, last, s.r0 * p.c.n_heads + head, R);
+      if (p.by_unit)
+        p.cuts[b * p.c.n_heads + head] = cut;
+      else if (!whole)
+        p.cuts[blockIdx.x] = cut;
+      told |= !whole;
+    }
     if (threadIdx.x < R) {
       const int r = threadIdx.x;
-      float mm = -CUDART_INF_F, ll = 0.0f;
+      float mm = kNoMax, ll = 0.0f;
 #pragma unroll
       for (int i = 0; i < kDecWarps; ++i) mm = fmaxf(mm, ml_s[i][r].x);
 #pragma unroll
       for (int i = 0; i < kDecWarps; ++i) {
-        const float f = ml_s[i][r].x == -CUDART_INF_F ? 0.0f : ex2(ml_s[i][r].x - mm);
+        const float f = ex2(ml_s[i][r].x - mm);
         f_s[i][r] = f;
         ll += ml_s[i][r].y * f;
       }
@@ -388,7 +507,7 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 4 : 3) attention_decode
               ll > 0.0f ? (mm - kShift) * kLn2 + logf(ll) : -CUDART_INF_F;
         }
       } else {
-        p.part_ml[slot * kRows + r] = make_float2(mm, ll);
+        p.part_ml[static_cast<int64_t>(slot) * kRows + r] = make_float2(mm, ll);
       }
     }
     __syncthreads();
@@ -406,74 +525,74 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 4 : 3) attention_decode
         const int64_t at = (static_cast<int64_t>(s.r0 + tok) * p.hq + head * p.group + (r - tok * p.group)) * D;
         reinterpret_cast<uint2*>(p.out + at)[d] = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
       } else {
-        reinterpret_cast<float4*>(p.part_o + (slot * kRows + r) * D)[d] = x;
+        reinterpret_cast<float4*>(p.part_o + (static_cast<int64_t>(slot) * kRows + r) * D)[d] = x;
       }
     }
     __syncthreads();
     w += tile1 - tile0;
   }
+  if (!p.by_unit && threadIdx.x == 0 && !told) p.cuts[blockIdx.x] = make_int4(-1, 0, 0, 0);
 }
 
-// Joins the partial sums of the units that the runs of n_cta CTAs cut: block
-// (c, y) takes rows y, y + gridDim.y, ... of the unit whose first cut is the
-// start of run c + 1.  Four groups of D threads each take a quarter of the
-// partials.
+// Joins the partial sums of a unit that several runs share: block (x, y) takes
+// rows of the unit that cut x names.  Groups of D threads take a row each
+// where there are few partials, else they share a row's.
+constexpr int kJoinThreads = 512;
+
 template <int D, int NT>
-__global__ void __launch_bounds__(4 * D) attention_combine_kernel(AttnArgs p, int n_cta, int min_quota) {
-  constexpr int kRows = 8 * NT;
-  __shared__ DecPlan<4 * D> plan;
-  __shared__ float o_s[4][D];
-  __shared__ float2 ml_s[4];
-  const long long total = plan.total(p);
-  const long long quota = dec_quota(total, n_cta, min_quota);
-  const long long cut = quota * (blockIdx.x + 1);
-  if (cut < total) plan.find(p, cut);
+__global__ void __launch_bounds__(kJoinThreads) attention_combine_kernel(AttnArgs p) {
+  constexpr int kRows = 8 * NT, kGroups = kJoinThreads / D;
+  __shared__ float o_s[kGroups][D];
+  __shared__ float2 ml_s[kGroups];
   // every block waits for the sums, also one that has none to join, so that
   // this kernel's end comes after the first one's
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (cut >= total) return;
-  const SeqInfo s = seq_info(p, plan.b);
-  const int nt = dec_tiles(s);
-  const int head = static_cast<int>((cut - plan.base) / nt);
-  const long long first = plan.base + static_cast<long long>(head) * nt, last = first + nt;
-  if (first == cut || cut - quota > first) return;
-  const int c0 = blockIdx.x, c1 = static_cast<int>((last - 1) / quota);
-  const int R = min(s.nq * p.group, kRows);
+  const int4 cut = __ldcg(p.cuts + blockIdx.x);          // slot of the first part, last run, place, rows
+  if (cut.x < 0) return;
+  const int c0 = cut.x >> 1, n = cut.y - c0 + 1, R = cut.w;
+  const int r0 = cut.z / p.c.n_heads, head = cut.z - r0 * p.c.n_heads;
   const int grp = threadIdx.x / D, d = threadIdx.x - grp * D;
-  for (int r = blockIdx.y; r < R; r += gridDim.y) {
-    float m = -CUDART_INF_F, l = 0.0f, o = 0.0f;
-#pragma unroll 4
-    for (int c = c0 + grp; c <= c1; c += 4) {
-      // the unit's first run ends with it (slot 1) unless it begins with it
-      const int64_t slot = 2 * static_cast<int64_t>(c) + ((c == c0 && first != c0 * quota) ? 1 : 0);
-      const float2 ml = __ldcg(p.part_ml + slot * kRows + r);
-      const float y = __ldcg(p.part_o + (slot * kRows + r) * D + d);
-      const float mn = fmaxf(m, ml.x);
-      const float a = m == -CUDART_INF_F ? 0.0f : ex2(m - mn), f = ml.x == -CUDART_INF_F ? 0.0f : ex2(ml.x - mn);
-      m = mn;
-      l = l * a + ml.y * f;
-      o = o * a + y * f;
-    }
-    o_s[grp][d] = o;
-    if (d == 0) ml_s[grp] = make_float2(m, l);
-    __syncthreads();
-    if (grp == 0) {
-      float mm = -CUDART_INF_F, ll = 0.0f, oo = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) mm = fmaxf(mm, ml_s[i].x);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float f = ml_s[i].x == -CUDART_INF_F ? 0.0f : ex2(ml_s[i].x - mm);
-        ll += ml_s[i].y * f;
-        oo += o_s[i][d] * f;
+  const bool shared = n > 8;
+  const int i0 = shared ? grp : 0, step = shared ? kGroups : 1;
+  for (int rb = blockIdx.y * (shared ? 1 : kGroups); rb < R; rb += gridDim.y * (shared ? 1 : kGroups)) {
+    const int r = shared ? rb : rb + grp;
+    float m = kNoMax, l = 0.0f, o = 0.0f;
+    if (r < R) {
+#pragma unroll 8
+      for (int i = i0; i < n; i += step) {
+        // the unit's first part, then the first of each later run
+        const int64_t at = static_cast<int64_t>(i == 0 ? cut.x : 2 * (c0 + i)) * kRows + r;
+        const float2 ml = __ldcg(p.part_ml + at);
+        const float y = __ldcg(p.part_o + at * D + d);
+        const float mn = fmaxf(m, ml.x), a = ex2(m - mn), f = ex2(ml.x - mn);
+        m = mn;
+        l = l * a + ml.y * f;
+        o = o * a + y * f;
       }
-      const int tok = static_cast<int>(fast_div(r, p.group_div));
-      const int64_t row = static_cast<int64_t>(s.r0 + tok) * p.hq + head * p.group + (r - tok * p.group);
-      const float inv = ll > 0.0f ? kScaleUnit * __ldg(p.c.g_v + head) / ll : 0.0f;
-      p.out[row * D + d] = static_cast<uint16_t>(float_to_bf16_bits(oo * inv));
-      if (d == 0 && p.lse != nullptr) p.lse[row] = ll > 0.0f ? (mm - kShift) * kLn2 + logf(ll) : -CUDART_INF_F;
     }
-    __syncthreads();
+    if (shared) {
+      o_s[grp][d] = o;
+      if (d == 0) ml_s[grp] = make_float2(m, l);
+      __syncthreads();
+      if (grp == 0) {
+#pragma unroll
+        for (int k = 1; k < kGroups; ++k) {
+          const float2 ml = ml_s[k];
+          const float mn = fmaxf(m, ml.x), a = ex2(m - mn), f = ex2(ml.x - mn);
+          m = mn;
+          l = l * a + ml.y * f;
+          o = o * a + o_s[k][d] * f;
+        }
+      }
+    }
+    if (r < R && (!shared || grp == 0)) {
+      const int tok = static_cast<int>(fast_div(r, p.group_div));
+      const int64_t row = static_cast<int64_t>(r0 + tok) * p.hq + head * p.group + (r - tok * p.group);
+      const float inv = l > 0.0f ? kScaleUnit * __ldg(p.c.g_v + head) / l : 0.0f;
+      p.out[row * D + d] = static_cast<uint16_t>(float_to_bf16_bits(o * inv));
+      if (d == 0 && p.lse != nullptr) p.lse[row] = l > 0.0f ? (m - kShift) * kLn2 + logf(l) : -CUDART_INF_F;
+    }
+    if (shared) __syncthreads();
   }
 }
 

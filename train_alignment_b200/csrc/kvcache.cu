@@ -20,6 +20,8 @@ int check_cache(const quads_kv_cache* c) {
                 "head_dim (%d) must be 64 or 128", c->head_dim);
   QUADS_REQUIRE(c->page_size >= 16 && c->page_size <= 65536 && c->page_size % 16 == 0, QUADS_ERR_UNSUPPORTED_SHAPE,
                 "page_size (%d) must be a multiple of 16 in [16, 65536]", c->page_size);
+  QUADS_REQUIRE(c->n_pages * c->n_heads * c->page_size < (int64_t(1) << 32) - 1, QUADS_ERR_UNSUPPORTED_SHAPE,
+                "n_pages * n_heads * page_size must be below 2^32 - 1");
   QUADS_REQUIRE(c->n_pages == 0 || (c->k_codes && c->k_scales && c->v_codes && c->v_scales), QUADS_ERR_INVALID_ARG,
                 "null cache pointer");
   QUADS_REQUIRE(c->g_k && c->g_v, QUADS_ERR_INVALID_ARG, "null decode scales");
