@@ -2,72 +2,30 @@
 //
 //   out[r][h] = sum_j softmax_j(scale q[r][h] . k_j) v_j,  j <= p, j > p - window
 //
-// One warp per (row, query head): an online softmax over the positions in
-// order, 32 positions' scores at a time.
-#include "attention.cuh"
+// Two kernels: few rows per sequence and key head (attention_decode.cuh) are
+// bound by the cache's bytes, many (attention_chunk.cuh) by the tensor cores.
+#include "attention_chunk.cuh"
 #include "attention_decode.cuh"
 
 namespace quads {
-namespace {
 
-template <int D>
-__global__ void __launch_bounds__(128) attention_kernel(AttnArgs p) {
-  const int lane = threadIdx.x & 31;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  const int64_t r = item / p.hq;
-  if (r >= p.rows) return;
-  const int h = static_cast<int>(item - r * p.hq), hk = h / p.group;
-  const int b = warp_find_seq(p.off, p.c.n_seqs, static_cast<int>(r), lane);
-  if (b < 0) return;
-  const int r0 = p.off[b], r1 = p.off[b + 1];
-  if (r >= r1 || r - r0 >= p.max_q) return;
-  const int len = p.kv_len[b];
-  const int64_t pos = static_cast<int64_t>(len) - (r1 - r0) + (r - r0);
-  constexpr int kE = D / 32;                          // elements of a lane
-  float q[kE], acc[kE], m = -CUDART_INF_F, l = 0.0f;
-#pragma unroll
-  for (int i = 0; i < kE; ++i) {
-    q[i] = bf16_bits_to_float(p.q[r * p.ld_q + h * D + lane * kE + i]);
-    acc[i] = 0.0f;
-  }
-  const float gk = p.c.g_k[hk], gv = p.c.g_v[hk];
-  const int64_t lo64 = p.window > 0 ? pos - p.window + 1 : 0;
-  const int lo = static_cast<int>(lo64 > 0 ? lo64 : 0);
-  for (int j = lo; j <= pos; ++j) {
-    int at;
-    const int page = page_of(p.c, b, j, at);
-    if (page < 0) continue;
-    const int64_t row = cache_row(p.c, page, hk, at);
-    float s = 0.0f, v[kE];
-    const float ks = e4m3_value(p.c.k_scales[row * (D / 16) + lane * kE / 16]) * gk;
-    const float vs = e4m3_value(p.c.v_scales[row * (D / 16) + lane * kE / 16]) * gv;
-#pragma unroll
-    for (int i = 0; i < kE; ++i) {
-      const int e = lane * kE + i;
-      s += q[i] * (e2m1_value((p.c.k_codes[row * (D / 2) + e / 2] >> (4 * (e & 1))) & 15u) * ks);
-      v[i] = e2m1_value((p.c.v_codes[row * (D / 2) + e / 2] >> (4 * (e & 1))) & 15u) * vs;
-    }
-#pragma unroll
-    for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-    s *= p.scale;
-    const float mn = fmaxf(m, s), a = m == -CUDART_INF_F ? 0.0f : __expf(m - mn), w = __expf(s - mn);
-    m = mn;
-    l = l * a + w;
-#pragma unroll
-    for (int i = 0; i < kE; ++i) acc[i] = acc[i] * a + w * v[i];
-  }
-  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-#pragma unroll
-  for (int i = 0; i < kE; ++i)
-    p.out[(r * p.hq + h) * D + lane * kE + i] = static_cast<uint16_t>(float_to_bf16_bits(acc[i] * inv));
-  if (p.lse != nullptr && lane == 0) p.lse[r * p.hq + h] = l > 0.0f ? m + logf(l) : -CUDART_INF_F;
+int attention_wait_status(unsigned int* v) {
+  if (cudaMemcpyFromSymbol(v, g_attention_wait_status, sizeof(*v)) != cudaSuccess)
+    return set_error(QUADS_ERR_CUDA, "cannot read the device status word");
+  const unsigned int zero = 0;
+  if (*v && cudaMemcpyToSymbol(g_attention_wait_status, &zero, sizeof(zero)) != cudaSuccess)
+    return set_error(QUADS_ERR_CUDA, "cannot clear the device status word");
+  return QUADS_OK;
 }
+
+namespace {
 
 // CTAs of the kernel for few rows: as many as are resident at once.
 int dec_grid(int nt) {
   const int n = dec_ctas_per_sm(nt) * num_sms();
   return n < kMaxRuns ? n : kMaxRuns;
 }
+constexpr int kChMinTiles = 4;       // key tiles of a split: shorter ones cost more in joining than they save
 constexpr int kDecMinQuota = 4;      // tiles of a run: shorter ones cost more in joining than they save
 
 size_t dec_workspace(int D, int nt) {
@@ -101,6 +59,48 @@ int launch_decode(AttnArgs p, void* ws, int unit_rows, cudaStream_t stream) {
   return QUADS_OK;
 }
 
+// The grid of the kernel for many rows: blocks of 256 rows (at most; some
+// find no rows), and the splits of their keys that fill the SMs.
+struct ChunkPlan {
+  int64_t blocks;
+  int n_split;
+};
+ChunkPlan chunk_plan(const quads_kv_cache* c, int64_t rows, int heads_q, int n_seqs, int max_pages, int max_q_len) {
+  const int64_t group = heads_q / c->n_heads;
+  const int64_t by_rows = rows * group / kChRows + n_seqs;
+  const int64_t by_seqs = ceil_div(static_cast<int64_t>(max_q_len) * group, int64_t(kChRows)) * n_seqs;
+  ChunkPlan p{by_rows < by_seqs ? by_rows : by_seqs, 1};
+  const int64_t units = p.blocks * c->n_heads;
+  const int64_t tiles = ceil_div(static_cast<int64_t>(max_pages) * c->page_size, int64_t(kChTile));
+  int64_t n = units > 0 ? num_sms() / units : 1;
+  if (n > tiles / kChMinTiles) n = tiles / kChMinTiles;
+  if (n > 1) p.n_split = static_cast<int>(n);
+  return p;
+}
+
+size_t chunk_workspace(const quads_kv_cache* c, int64_t rows, int heads_q, int n_split) {
+  if (n_split <= 1) return 0;
+  return static_cast<size_t>(n_split) * rows * heads_q * (c->head_dim * sizeof(float) + sizeof(float2));
+}
+
+template <int D>
+int launch_chunk(AttnArgs p, const ChunkPlan& plan, void* ws, cudaStream_t stream) {
+  p.part_o = static_cast<float*>(ws);
+  p.part_ml = reinterpret_cast<float2*>(p.part_o + static_cast<size_t>(plan.n_split) * p.rows * p.hq * D);
+  const int smem = ch_smem_bytes(D);
+  if (cudaFuncSetAttribute(attention_chunk_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+    return check_launch("attention_chunk_kernel attributes");
+  const dim3 grid(static_cast<unsigned>(plan.blocks * p.c.n_heads), plan.n_split);
+  attention_chunk_kernel<D><<<grid, kChThreads, smem, stream>>>(p, plan.n_split);
+  count_launches(1);
+  QUADS_TRY(check_launch("attention_chunk_kernel"));
+  if (plan.n_split > 1) {
+    attention_join_kernel<D><<<static_cast<unsigned>(ceil_div(p.rows * p.hq, int64_t(8))), 256, 0, stream>>>(p, plan.n_split);
+    count_launches(1);
+  }
+  return check_launch("attention_join_kernel");
+}
+
 }  // namespace
 }  // namespace quads
 
@@ -111,10 +111,10 @@ extern "C" {
 size_t quads_attention_paged_workspace_bytes(const quads_kv_cache* cache, int64_t rows, int heads_q, int n_seqs,
                                              int max_pages, int max_q_len) {
   if (cache == nullptr || cache->n_heads < 1 || heads_q < 1 || heads_q % cache->n_heads != 0) return 0;
-  (void)rows; (void)n_seqs; (void)max_pages;
+  if (rows <= 0 || n_seqs <= 0 || max_q_len <= 0 || max_pages < 0) return 0;
   const int64_t unit_rows = static_cast<int64_t>(max_q_len) * (heads_q / cache->n_heads);
   if (unit_rows <= 16) return dec_workspace(cache->head_dim, unit_rows <= 8 ? 1 : 2);
-  return 0;
+  return chunk_workspace(cache, rows, heads_q, chunk_plan(cache, rows, heads_q, n_seqs, max_pages, max_q_len).n_split);
 }
 
 int quads_attention_paged(const uint16_t* q, int64_t rows, int64_t ld_q, int heads_q, const quads_kv_cache* cache,
@@ -155,13 +155,10 @@ int quads_attention_paged(const uint16_t* q, int64_t rows, int64_t ld_q, int hea
       return n <= 8 ? launch_decode<64, 1>(p, ws, n, stream) : launch_decode<64, 2>(p, ws, n, stream);
     return n <= 8 ? launch_decode<128, 1>(p, ws, n, stream) : launch_decode<128, 2>(p, ws, n, stream);
   }
-  const unsigned grid = static_cast<unsigned>(ceil_div(rows * heads_q, int64_t(4)));
-  if (cache->head_dim == 64)
-    attention_kernel<64><<<grid, 128, 0, stream>>>(p);
-  else
-    attention_kernel<128><<<grid, 128, 0, stream>>>(p);
-  count_launches(1);
-  return check_launch("attention_kernel");
+  const ChunkPlan plan = chunk_plan(cache, rows, heads_q, n_seqs, max_pages, max_q_len);
+  QUADS_REQUIRE(plan.blocks * cache->n_heads < (int64_t(1) << 31) && ceil_div(rows * heads_q, int64_t(8)) < (int64_t(1) << 31),
+                QUADS_ERR_UNSUPPORTED_SHAPE, "too many rows");
+  return cache->head_dim == 64 ? launch_chunk<64>(p, plan, ws, stream) : launch_chunk<128>(p, plan, ws, stream);
 }
 
 }  // extern "C"

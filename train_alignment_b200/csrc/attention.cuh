@@ -94,6 +94,10 @@ __device__ __forceinline__ uint32_t scale_pair_f16x2(uint32_t s0, uint32_t s1) {
 }
 constexpr float kScaleUnit = 256.0f;      // what the 2^-8 above is undone with
 
+constexpr uint32_t kNoRow = 0xFFFFFFFFu;     // in place of a cache row: no page
+constexpr float kNoMax = -1e30f;             // the running maximum before the first key: finite, so that
+                                             // differences of maxima are never NaN
+
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 // A row's running maximum may fall this far (in powers of two) behind a new

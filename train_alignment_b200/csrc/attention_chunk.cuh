@@ -1,0 +1,534 @@
+// Attention of many rows (chunks of prompts, groups of more than 16 rows):
+// bound by the tensor cores and by the exponentials.
+//
+// A CTA takes 256 rows (two tiles of 128) of one key head: row r of a
+// sequence is query head r % group of its token r / group, so the rows share
+// every key.  Keys come in tiles of 128:
+//   warps 8..11   convert a tile's E2M1 codes and E4M3 scales to FP16 (exact:
+//                 at most 6 significant bits) in shared memory, a token per
+//                 thread, keys and values in the same 128-byte-swizzled rows;
+//   warp 12       issues S_i = Q_i K^T and O_i += P_i V (tcgen05, FP16
+//                 operands, FP32 accumulators in tensor memory; V is read as
+//                 the matrix whose reduction runs over its rows);
+//   warps 0..3, 4..7  own tile 0 and 1, a row per thread: the maximum of S_i,
+//                 then exp(S_i - m) as FP16 over S_i's own columns (the A
+//                 operand of the second product), the row's sum in FP32.
+// The two tiles alternate, so one's products run during the other's
+// exponentials.  O_i is rescaled only when a row's maximum has grown by more
+// than 2^kLag since the last time.
+// Tensor memory: S_0, S_1 at columns 0 and 128 (P_i in the first 64 of them),
+// O_0, O_1 at 256 and 384.
+//
+// Where the rows give fewer CTAs than SMs the keys are split too, and
+// attention_join_kernel joins the parts.  Every wait is bounded.
+#pragma once
+
+#include "attention.cuh"
+#include "sm100.cuh"
+
+namespace quads {
+
+constexpr int kChTile = 128;                     // rows of a tile, keys of a tile
+constexpr int kChRows = 2 * kChTile;
+constexpr int kChSoftWarps = 8;
+constexpr int kChConvWarp = 8, kChConvWarps = 4;
+constexpr int kChMmaWarp = 12;
+constexpr int kChThreads = 32 * (kChMmaWarp + 1);
+constexpr int kChStages = 2;
+constexpr uint32_t kChOCol = 256;
+constexpr uint64_t kChTimeoutNs = 4000000000ull, kChDrainNs = 500000000ull;
+__host__ __device__ constexpr int ch_tile_bytes(int D) { return kChTile * D * 2; }
+__host__ __device__ constexpr int ch_smem_bytes(int D) { return 1024 + (2 + 2 * kChStages) * ch_tile_bytes(D) + 256; }
+
+// kind::f16 with FP16 operands and FP32 accumulators; trans_b: B's rows run
+// along the reduction.
+__host__ __device__ constexpr uint32_t idesc_f16(int n, bool trans_b) {
+  return (1u << 4) | (trans_b ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(kChTile >> 4) << 24);
+}
+// B operand whose rows run along the reduction: 128-byte swizzled rows of 64
+// elements, 8-row groups 1024 bytes apart, the next 64 elements 16 KB on.
+__device__ __forceinline__ uint64_t desc_rows_sw128(uint32_t addr) {
+  return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | (static_cast<uint64_t>((kChTile * 128) >> 4) << 16) |
+         (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
+}
+
+// Set by a wait that gave up; read and cleared by quads_device_status().
+__device__ unsigned int g_attention_wait_status = 0u;
+
+__device__ __forceinline__ bool ch_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                        uint64_t limit_ns = kChTimeoutNs) {
+  if (mbar_test(bar, parity)) return true;
+  const uint64_t t0 = global_timer();
+  while (true) {
+    if (mbar_test(bar, parity)) return true;
+    if (abort_flag != nullptr && *abort_flag) return false;
+    if (global_timer() - t0 > limit_ns) {
+      if (abort_flag != nullptr) *abort_flag = 1;
+      atomicOr(&g_attention_wait_status, 1u);
+      return false;
+    }
+  }
+}
+
+__device__ __forceinline__ void tmem_store32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+
+// Rows of one CTA and the keys that they see.
+struct ChUnit {
+  SeqInfo s;
+  int head;
+  int row0;          // first row (of the sequence's nq * group)
+  int t0, t1;        // key tiles of the CTA: [s.lo + 128 t0, s.lo + 128 t1)
+};
+
+// Key tiles (counted from s.lo) that rows [row0, row0 + n) see: [a, b).
+__device__ __forceinline__ void ch_range(const AttnArgs& p, const SeqInfo& s, int row0, int n, int& a, int& b) {
+  const int last = min(row0 + n, s.nq * p.group) - 1;
+  if (last < row0) { a = b = 0; return; }
+  const int pos_a = s.pos0 + static_cast<int>(fast_div(row0, p.group_div));
+  const int pos_b = s.pos0 + static_cast<int>(fast_div(last, p.group_div));
+  const int hi = max(min(s.hi, pos_b + 1), s.lo);
+  const int lo = min(max(p.window > 0 ? pos_a - p.window + 1 : 0, s.lo), hi);
+  a = (lo - s.lo) / kChTile;
+  b = (hi - s.lo + kChTile - 1) / kChTile;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kChThreads, 1) attention_chunk_kernel(AttnArgs p, int n_split) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_addr(smem_raw), base = (raw + 1023u) & ~1023u;
+  uint8_t* const base_ptr = smem_raw + (base - raw);
+  constexpr int kTB = ch_tile_bytes(D);
+  const uint32_t q_s = base, k_s = base + 2 * kTB, v_s = k_s + kChStages * kTB;
+  const uint32_t bar0 = v_s + kChStages * kTB;
+  const uint32_t q_full = bar0, drain = bar0 + 8;
+  auto k_full = [&](int s) { return bar0 + 16 + 8u * s; };
+  auto k_empty = [&](int s) { return bar0 + 32 + 8u * s; };
+  auto v_full = [&](int s) { return bar0 + 48 + 8u * s; };
+  auto v_empty = [&](int s) { return bar0 + 64 + 8u * s; };
+  auto s_full = [&](int i) { return bar0 + 80 + 8u * i; };
+  auto p_full = [&](int i) { return bar0 + 96 + 8u * i; };
+  auto o_full = [&](int i) { return bar0 + 112 + 8u * i; };
+  uint8_t* const misc = base_ptr + (bar0 + 128 - base);
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(misc);
+  volatile int* const abort_flag = reinterpret_cast<volatile int*>(misc + 4);
+  volatile uint32_t* const gone_s = reinterpret_cast<volatile uint32_t*>(misc + 8);   // [8]: groups of 16 keys without a page
+  int* const unit_s = reinterpret_cast<int*>(misc + 40);                             // {sequence, block}
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // the block'th 256 rows, counted through the sequences
+  const int block = static_cast<int>(blockIdx.x) / p.c.n_heads;
+  if (warp == 0) {
+    int run = 0, found = -1, at = 0;
+    for (int c0 = 0; c0 < p.c.n_seqs && found < 0; c0 += 32) {
+      int n = 0;
+      if (c0 + lane < p.c.n_seqs) {
+        const SeqInfo s = seq_info(p, c0 + lane);
+        n = (s.nq * p.group + kChRows - 1) / kChRows;
+      }
+      int incl = n;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += v;
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, block < run + incl);
+      if (hit) {
+        const int l = __ffs(hit) - 1;
+        found = c0 + l;
+        // later rows see more keys: the longest blocks of a sequence first
+        at = run + __shfl_sync(0xffffffffu, incl, l) - 1 - block;
+      }
+      run += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (lane == 0) {
+      unit_s[0] = found;
+      unit_s[1] = at;
+    }
+  }
+  if (threadIdx.x == 32) {
+    mbar_init(q_full, kChSoftWarps);
+    mbar_init(drain, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(k_full(i), kChConvWarps);
+      mbar_init(k_empty(i), 1);
+      mbar_init(v_full(i), kChConvWarps);
+      mbar_init(v_empty(i), 1);
+      mbar_init(s_full(i), 1);
+      mbar_init(p_full(i), kChSoftWarps / 2);
+      mbar_init(o_full(i), 1);
+    }
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kChMmaWarp) {
+    tmem_alloc(smem_addr(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  const int b = unit_s[0];
+  if (b >= 0) {
+    ChUnit u;
+    u.s = seq_info(p, b);
+    u.head = static_cast<int>(blockIdx.x) - block * p.c.n_heads;
+    u.row0 = unit_s[1] * kChRows;
+    // this split's key tiles, and those of each row tile among them
+    int ta[2], tb[2];
+    ch_range(p, u.s, u.row0, kChTile, ta[0], tb[0]);
+    ch_range(p, u.s, u.row0 + kChTile, kChTile, ta[1], tb[1]);
+    const bool two = u.row0 + kChTile < u.s.nq * p.group;
+    u.t0 = two ? min(ta[0], ta[1]) : ta[0];
+    u.t1 = two ? max(tb[0], tb[1]) : tb[0];
+    if (n_split > 1) {
+      const int per = (u.t1 - u.t0 + n_split - 1) / n_split;
+      u.t0 = min(u.t1, u.t0 + per * static_cast<int>(blockIdx.y));
+      u.t1 = min(u.t1, u.t0 + per);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      ta[i] = max(ta[i], u.t0);
+      tb[i] = max(min(tb[i], u.t1), ta[i]);
+    }
+
+    if (warp < kChSoftWarps) {
+      // ------------------------------------------------- softmax, a row each
+      const int i = warp >> 2, r = threadIdx.x & 127;
+      const int row = u.row0 + i * kChTile + r;
+      const bool valid = row < u.s.nq * p.group;
+      const int tok = valid ? static_cast<int>(fast_div(row, p.group_div)) : 0;
+      const int head_q = u.head * p.group + (valid ? row - tok * p.group : 0);
+      float c2;
+      {
+        // the row's queries, scaled by a power of two, as FP16
+        const uint4* src = reinterpret_cast<const uint4*>(p.q + static_cast<int64_t>(u.s.r0 + tok) * p.ld_q + head_q * D);
+        uint4 x[D / 8];
+        uint32_t mx = 0;
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j) {
+          x[j] = valid ? __ldg(src + j) : make_uint4(0, 0, 0, 0);
+          mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(x[j].x & 0x7FFF7FFFu, x[j].y & 0x7FFF7FFFu),
+                                     __vmaxu2(x[j].z & 0x7FFF7FFFu, x[j].w & 0x7FFF7FFFu)));
+        }
+        const uint32_t e = row_exponent(max(mx & 0xFFFFu, mx >> 16));
+        const float down = exp_field_down(e);
+        c2 = p.scale * kLog2e * kScaleUnit * __ldg(p.c.g_k + u.head) * exp_field_up(e);
+        const uint32_t dst = q_s + i * kTB + r * 128;
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j)
+          st_shared_v4(dst + (j >> 3) * (kChTile * 128) + (((j & 7) ^ (r & 7)) << 4), bf16x2_scaled_f16x2(x[j].x, down),
+                       bf16x2_scaled_f16x2(x[j].y, down), bf16x2_scaled_f16x2(x[j].z, down),
+                       bf16x2_scaled_f16x2(x[j].w, down));
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full);
+
+      const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+      const uint32_t s_col = tmem + lane_base + i * kChTile, o_col = tmem + lane_base + kChOCol + i * kChTile;
+      const int pos = u.s.pos0 + tok;
+      float up = kShift - kNoMax, l = 0.0f;
+      bool ok = true;
+      for (int t = ta[i]; t < tb[i]; ++t) {
+        ok = __all_sync(0xffffffffu, ch_wait(s_full(i), (t - ta[i]) & 1, abort_flag));
+        if (!ok) break;
+        tc_fence_after();
+        const int j0 = u.s.lo + t * kChTile;
+        // columns [first, last] of the tile are seen
+        const int last = valid ? min(pos, u.s.hi - 1) - j0 : -1;
+        const int first = p.window > 0 ? pos - p.window + 1 - j0 : 0;
+        uint32_t gone = gone_s[(t - u.t0) & 7];        // two bits in each byte: eight groups of 16 keys
+        gone = (gone & 3u) | ((gone >> 6) & 0xCu) | ((gone >> 12) & 0x30u) | ((gone >> 18) & 0xC0u);
+        const bool masked = __any_sync(0xffffffffu, last < kChTile - 1 || first > 0 || gone != 0);
+        float top = -CUDART_INF_F;                      // the largest exponent, with the maximum so far
+#pragma unroll
+        for (int c = 0; c < kChTile / 32; ++c) {
+          uint32_t x[32];
+          tmem_load32(s_col + 32 * c, x);
+          tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            const float y = __fmaf_rn(__uint_as_float(x[k]), c2, up);
+            if (masked) {
+              const int col = 32 * c + k;
+              if (col <= last && col >= first && !((gone >> (col >> 4)) & 1u)) top = fmaxf(top, y);
+            } else {
+              top = fmaxf(top, y);
+            }
+          }
+        }
+        if (__any_sync(0xffffffffu, top > kShift + kLag)) {
+          // a new maximum: the first tile's, or one that has grown by kLag
+          float mx = -CUDART_INF_F;
+#pragma unroll
+          for (int c = 0; c < kChTile / 32; ++c) {
+            uint32_t x[32];
+            tmem_load32(s_col + 32 * c, x);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+              const int col = 32 * c + k;
+              if (col <= last && col >= first && !((gone >> (col >> 4)) & 1u)) mx = fmaxf(mx, __uint_as_float(x[k]) * c2);
+            }
+          }
+          const float un = fminf(up, kShift - mx);
+          const float a = ex2(un - up);
+          up = un;
+          l *= a;
+          if (t > ta[i]) {                              // the products before are complete: S_i of this tile came after them
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t x[32];
+              tmem_load32(o_col + 32 * c, x);
+              tmem_wait_ld();
+#pragma unroll
+              for (int k = 0; k < 32; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * a);
+              tmem_store32(o_col + 32 * c, x);
+            }
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < kChTile / 32; ++c) {
+          uint32_t x[32], w[16];
+          tmem_load32(s_col + 32 * c, x);
+          tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            float y = __fmaf_rn(__uint_as_float(x[k]), c2, up);
+            if (masked) {
+              const int col = 32 * c + k;
+              if (!(col <= last && col >= first && !((gone >> (col >> 4)) & 1u))) y = -CUDART_INF_F;
+            }
+            x[k] = __float_as_uint(ex2(y));
+          }
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            l += __uint_as_float(x[2 * k]) + __uint_as_float(x[2 * k + 1]);
+            w[k] = pack_f16x2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1]));
+          }
+          tmem_store16(s_col + 16 * c, w);              // over columns of S that have been read
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full(i));
+      }
+      if (ok && tb[i] > ta[i]) ok = __all_sync(0xffffffffu, ch_wait(o_full(i), 0, abort_flag));
+      if (ok && (i == 0 || two)) {
+        tc_fence_after();
+        const bool some = tb[i] > ta[i];
+        const int64_t orow = static_cast<int64_t>(u.s.r0 + tok) * p.hq + head_q;
+        if (n_split > 1) {
+          const int64_t at = (static_cast<int64_t>(blockIdx.y) * p.rows + u.s.r0 + tok) * p.hq + head_q;
+          if (valid) p.part_ml[at] = make_float2(kShift - up, l);
+          if (some)
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t x[32];
+              tmem_load32(o_col + 32 * c, x);
+              tmem_wait_ld();
+              if (valid) {
+                uint4* dst = reinterpret_cast<uint4*>(p.part_o + at * D + 32 * c);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) dst[k] = make_uint4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+              }
+            }
+        } else {
+          const float inv = l > 0.0f ? kScaleUnit * __ldg(p.c.g_v + u.head) / l : 0.0f;
+          if (valid && p.lse != nullptr) p.lse[orow] = l > 0.0f ? -up * kLn2 + logf(l) : -CUDART_INF_F;
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t x[32];
+            if (some) {
+              tmem_load32(o_col + 32 * c, x);
+              tmem_wait_ld();
+            }
+            if (valid) {
+              uint4* dst = reinterpret_cast<uint4*>(p.out + orow * D + 32 * c);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                uint32_t w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const int y = 8 * k + 2 * e;
+                  // rows without a key: zeros, whatever the accumulator holds
+                  w[e] = l > 0.0f && some ? pack_bf16x2(__uint_as_float(x[y]) * inv, __uint_as_float(x[y + 1]) * inv) : 0u;
+                }
+                dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
+              }
+            }
+          }
+        }
+      }
+    } else if (warp < kChConvWarp + kChConvWarps) {
+      // -------------------------------------------- conversion, a token each
+      const int r = threadIdx.x - 32 * kChConvWarp;     // token of the tile
+      const int n = u.t1 - u.t0;
+      auto lookup = [&](int t) -> uint32_t {
+        const int j = u.s.lo + (u.t0 + t) * kChTile + r;
+        if (t >= n || j >= u.s.hi) return kNoRow;
+        int at;
+        const int page = page_of(p.c, b, j, at);
+        return page >= 0 ? static_cast<uint32_t>(cache_row(p.c, page, u.head, at)) : kNoRow;
+      };
+      uint4 kc[D / 32], vc[D / 32];
+      uint32_t ks[D / 64], vs[D / 64];
+      auto load = [&](const uint8_t* codes, const uint8_t* scales, uint32_t row, uint4 (&c)[D / 32], uint32_t (&s)[D / 64]) {
+        if (row == kNoRow) {
+#pragma unroll
+          for (int j = 0; j < D / 32; ++j) c[j] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int j = 0; j < D / 64; ++j) s[j] = 0;
+          return;
+        }
+        const uint4* src = reinterpret_cast<const uint4*>(codes + static_cast<uint64_t>(row) * (D / 2));
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) c[j] = __ldg(src + j);
+        const uint32_t* ss = reinterpret_cast<const uint32_t*>(scales + static_cast<uint64_t>(row) * (D / 16));
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j) s[j] = __ldg(ss + j);
+      };
+      auto convert = [&](uint32_t tile, const uint4 (&c)[D / 32], const uint32_t (&s)[D / 64]) {
+        const uint32_t dst = tile + r * 128;
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j) {               // 8 elements, one 16-byte chunk
+          const uint32_t word = (&c[j >> 2].x)[j & 3];
+          const uint32_t sc = scale_f16x2((s[j >> 3] >> (8 * ((j >> 1) & 3))) & 0x7Fu);
+          uint32_t h[4];
+          e2m1x8_to_f16x2(word, h);
+          st_shared_v4(dst + (j >> 3) * (kChTile * 128) + (((j & 7) ^ (r & 7)) << 4), hmul2_rn(h[0], sc), hmul2_rn(h[1], sc),
+                       hmul2_rn(h[2], sc), hmul2_rn(h[3], sc));
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+      };
+      uint32_t row = lookup(0), next = lookup(1);
+      load(p.c.k_codes, p.c.k_scales, row, kc, ks);
+      load(p.c.v_codes, p.c.v_scales, row, vc, vs);
+      for (int t = 0; t < n; ++t) {
+        const int st = t % kChStages;
+        const uint32_t free_parity = ((t / kChStages) & 1) ^ 1u;
+        if (!__all_sync(0xffffffffu, ch_wait(k_empty(st), free_parity, abort_flag))) break;
+        // groups of 16 keys without a page (those past the last key are masked by position)
+        const unsigned no = __ballot_sync(0xffffffffu, row == kNoRow);
+        if (lane == 0)
+          reinterpret_cast<volatile uint8_t*>(gone_s + (t & 7))[warp - kChConvWarp] =
+              static_cast<uint8_t>((no & 1u) | ((no >> 15) & 2u));
+        convert(k_s + st * kTB, kc, ks);
+        if (lane == 0) mbar_arrive(k_full(st));
+        const uint32_t after = lookup(t + 2);
+        load(p.c.k_codes, p.c.k_scales, next, kc, ks);
+        if (!__all_sync(0xffffffffu, ch_wait(v_empty(st), free_parity, abort_flag))) break;
+        convert(v_s + st * kTB, vc, vs);
+        if (lane == 0) mbar_arrive(v_full(st));
+        load(p.c.v_codes, p.c.v_scales, next, vc, vs);
+        row = next;
+        next = after;
+      }
+    } else if (lane == 0) {
+      // ----------------------------------------------------------------- MMA
+      constexpr uint32_t kIdQK = idesc_f16(kChTile, false), kIdPV = idesc_f16(D, true);
+      const int n = u.t1 - u.t0;
+      bool ok = ch_wait(q_full, 0, abort_flag);
+      auto active = [&](int i, int t) { return u.t0 + t >= ta[i] && u.t0 + t < tb[i]; };
+      auto scores = [&](int i, int t) {                 // S_i = Q_i K^T of tile t
+        const uint32_t kt = k_s + (t % kChStages) * kTB, qt = q_s + i * kTB;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t at = (kk >> 2) * (kChTile * 128) + (kk & 3) * 32;
+          mma_bf16(tmem + i * kChTile, desc_kmajor_sw128(qt + at), desc_kmajor_sw128(kt + at), kIdQK, kk != 0);
+        }
+        tc_commit(s_full(i));
+      };
+      if (n > 0 && ok) {
+        ok = ch_wait(k_full(0), 0, abort_flag);
+        tc_fence_after();
+        if (ok) {
+          for (int i = 0; i < 2; ++i)
+            if (active(i, 0)) scores(i, 0);
+          tc_commit(k_empty(0));
+        }
+      }
+      for (int t = 0; t < n && ok; ++t) {
+        const int st = t % kChStages;
+        const uint32_t parity = (t / kChStages) & 1;
+        ok = ch_wait(v_full(st), parity, abort_flag);
+        if (ok && t + 1 < n) ok = ch_wait(k_full((t + 1) % kChStages), ((t + 1) / kChStages) & 1, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        for (int i = 0; i < 2 && ok; ++i) {
+          if (active(i, t)) {
+            ok = ch_wait(p_full(i), (u.t0 + t - ta[i]) & 1, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t vt = v_s + st * kTB;
+#pragma unroll
+            for (int kk = 0; kk < kChTile / 16; ++kk)
+              mma_bf16_tmem_a(tmem + kChOCol + i * kChTile, tmem + i * kChTile + 8 * kk, desc_rows_sw128(vt + kk * 2048), kIdPV,
+                              (u.t0 + t > ta[i] || kk != 0) ? 1u : 0u);
+            if (u.t0 + t + 1 == tb[i]) tc_commit(o_full(i));
+          }
+          if (t + 1 < n && active(i, t + 1)) scores(i, t + 1);
+        }
+        if (!ok) break;
+        tc_commit(v_empty(st));
+        if (t + 1 < n) tc_commit(k_empty((t + 1) % kChStages));
+      }
+      // what was issued completes before the tensor memory is given back
+      tc_commit(drain);
+      ch_wait(drain, 0, nullptr, kChDrainNs);
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kChMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+// Joins the parts of rows whose keys were split: one warp per (row, head).
+template <int D>
+__global__ void __launch_bounds__(256) attention_join_kernel(AttnArgs p, int n_split) {
+  const int lane = threadIdx.x & 31;
+  const int64_t item = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  const int64_t r = item / p.hq;
+  if (r >= p.rows) return;
+  const int h = static_cast<int>(item - r * p.hq);
+  const int b = warp_find_seq(p.off, p.c.n_seqs, static_cast<int>(r), lane);
+  if (b < 0) return;
+  const SeqInfo s = seq_info(p, b);
+  if (r >= s.r0 + s.nq) return;
+  constexpr int kE = D / 32;
+  float m = kNoMax, l = 0.0f, o[kE];
+#pragma unroll
+  for (int e = 0; e < kE; ++e) o[e] = 0.0f;
+  for (int i = 0; i < n_split; ++i) {
+    const int64_t at = (static_cast<int64_t>(i) * p.rows + r) * p.hq + h;
+    const float2 ml = __ldcg(p.part_ml + at);
+    if (ml.y <= 0.0f) continue;                         // a part without keys has no sums
+    const float mn = fmaxf(m, ml.x), a = ex2(m - mn), f = ex2(ml.x - mn);
+    m = mn;
+    l = l * a + ml.y * f;
+#pragma unroll
+    for (int e = 0; e < kE; ++e) o[e] = o[e] * a + __ldcg(p.part_o + at * D + lane * kE + e) * f;
+  }
+  const float inv = l > 0.0f ? kScaleUnit * __ldg(p.c.g_v + h / p.group) / l : 0.0f;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + (r * p.hq + h) * D + lane * kE);
+#pragma unroll
+  for (int e = 0; e < kE / 2; ++e) dst[e] = pack_bf16x2(o[2 * e] * inv, o[2 * e + 1] * inv);
+  if (lane == 0 && p.lse != nullptr) p.lse[r * p.hq + h] = l > 0.0f ? (m - kShift) * kLn2 + logf(l) : -CUDART_INF_F;
+}
+
+}  // namespace quads

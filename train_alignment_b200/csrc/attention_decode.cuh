@@ -210,10 +210,6 @@ struct DecRaw {
   }
 };
 
-constexpr uint32_t kNoRow = 0xFFFFFFFFu;     // in place of a cache row: no page
-constexpr float kNoMax = -1e30f;             // the running maximum before the first key: finite, so that
-                                             // differences of maxima are never NaN
-
 template <int D, int NT>
 __global__ void __launch_bounds__(kDecThreads, dec_ctas_per_sm(NT)) attention_decode_kernel(AttnArgs p, int min_quota) {
   constexpr int kRows = 8 * NT;

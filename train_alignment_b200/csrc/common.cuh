@@ -25,6 +25,8 @@ int grid_sms();
 // Device address of the word in which bounded device-side waits record a
 // timeout (read and cleared by quads_device_status), or null.
 unsigned int* wait_status_word();
+// Reads and clears the attention kernels' own word.
+int attention_wait_status(unsigned int* v);
 
 // Returns QUADS_ERR_CUDA (with a message) if the last launch failed.
 int check_launch(const char* what);
