@@ -33,7 +33,9 @@ constexpr int kChRows = 2 * kChTile;
 constexpr int kChSoftWarps = 8;
 constexpr int kChConvWarp = 8, kChConvWarps = 4;
 constexpr int kChMmaWarp = 12;
-constexpr int kChThreads = 32 * (kChMmaWarp + 1);
+constexpr int kChThreads = 512;                  // four warpgroups of 128 registers a thread, which they share out:
+constexpr int kChSoftRegs = 192, kChConvRegs = 88, kChMmaRegs = 40;
+static_assert(2 * kChSoftRegs + kChConvRegs + kChMmaRegs <= 4 * 128, "registers of the four warpgroups");
 constexpr int kChStages = 2;
 constexpr uint32_t kChOCol = 256;
 constexpr uint64_t kChTimeoutNs = 4000000000ull, kChDrainNs = 500000000ull;
@@ -80,6 +82,41 @@ __device__ __forceinline__ void tmem_store32(uint32_t taddr, const uint32_t (&r)
       "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
+}
+
+template <int kRegs>
+__device__ __forceinline__ void regs_grow() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void regs_shrink() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+// 32 columns of this warp's lanes, without waiting for them.
+template <int kAt, int kN>
+__device__ __forceinline__ void tmem_load32_at(uint32_t taddr, float (&r)[kN]) {
+  uint32_t x[32];
+  tmem_load32(taddr, x);
+#pragma unroll
+  for (int i = 0; i < 32; ++i) r[kAt + i] = __uint_as_float(x[i]);
+}
+__device__ __forceinline__ uint64_t ffma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t fadd2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float fmax3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+
+// Bits first .. last of 32 columns that start at column c (first <= last or none).
+__device__ __forceinline__ uint32_t column_mask(int first, int last, int c) {
+  const int a = max(first - c, 0), b = min(last - c, 31);
+  if (a > b) return 0u;
+  return (0xFFFFFFFFu << a) & (0xFFFFFFFFu >> (31 - b));
 }
 
 // Rows of one CTA and the keys that they see.
@@ -205,6 +242,7 @@ __global__ void __launch_bounds__(kChThreads, 1) attention_chunk_kernel(AttnArgs
 
     if (warp < kChSoftWarps) {
       // ------------------------------------------------- softmax, a row each
+      regs_grow<kChSoftRegs>();
       const int i = warp >> 2, r = threadIdx.x & 127;
       const int row = u.row0 + i * kChTile + r;
       const bool valid = row < u.s.nq * p.group;
@@ -224,13 +262,16 @@ __global__ void __launch_bounds__(kChThreads, 1) attention_chunk_kernel(AttnArgs
         }
         const uint32_t e = row_exponent(max(mx & 0xFFFFu, mx >> 16));
         const float down = exp_field_down(e);
+        // the factor of the row's scores (to powers of two), positive: its sign goes to the queries
         c2 = p.scale * kLog2e * kScaleUnit * __ldg(p.c.g_k + u.head) * exp_field_up(e);
+        const float sign = c2 < 0.0f ? -down : down;
+        c2 = fmaxf(fabsf(c2), 1e-37f);                  // not zero, which times -inf were NaN
         const uint32_t dst = q_s + i * kTB + r * 128;
 #pragma unroll
         for (int j = 0; j < D / 8; ++j)
-          st_shared_v4(dst + (j >> 3) * (kChTile * 128) + (((j & 7) ^ (r & 7)) << 4), bf16x2_scaled_f16x2(x[j].x, down),
-                       bf16x2_scaled_f16x2(x[j].y, down), bf16x2_scaled_f16x2(x[j].z, down),
-                       bf16x2_scaled_f16x2(x[j].w, down));
+          st_shared_v4(dst + (j >> 3) * (kChTile * 128) + (((j & 7) ^ (r & 7)) << 4), bf16x2_scaled_f16x2(x[j].x, sign),
+                       bf16x2_scaled_f16x2(x[j].y, sign), bf16x2_scaled_f16x2(x[j].z, sign),
+                       bf16x2_scaled_f16x2(x[j].w, sign));
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -252,74 +293,67 @@ __global__ void __launch_bounds__(kChThreads, 1) attention_chunk_kernel(AttnArgs
         uint32_t gone = gone_s[(t - u.t0) & 7];        // two bits in each byte: eight groups of 16 keys
         gone = (gone & 3u) | ((gone >> 6) & 0xCu) | ((gone >> 12) & 0x30u) | ((gone >> 18) & 0xC0u);
         const bool masked = __any_sync(0xffffffffu, last < kChTile - 1 || first > 0 || gone != 0);
-        float top = -CUDART_INF_F;                      // the largest exponent, with the maximum so far
-#pragma unroll
-        for (int c = 0; c < kChTile / 32; ++c) {
-          uint32_t x[32];
-          tmem_load32(s_col + 32 * c, x);
-          tmem_wait_ld();
-#pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            const float y = __fmaf_rn(__uint_as_float(x[k]), c2, up);
-            if (masked) {
-              const int col = 32 * c + k;
-              if (col <= last && col >= first && !((gone >> (col >> 4)) & 1u)) top = fmaxf(top, y);
-            } else {
-              top = fmaxf(top, y);
-            }
-          }
-        }
-        if (__any_sync(0xffffffffu, top > kShift + kLag)) {
-          // a new maximum: the first tile's, or one that has grown by kLag
-          float mx = -CUDART_INF_F;
+        float x[kChTile];
+        tmem_load32_at<0>(s_col, x);
+        tmem_load32_at<32>(s_col + 32, x);
+        tmem_load32_at<64>(s_col + 64, x);
+        tmem_load32_at<96>(s_col + 96, x);
+        tmem_wait_ld();
+        if (masked) {
 #pragma unroll
           for (int c = 0; c < kChTile / 32; ++c) {
-            uint32_t x[32];
-            tmem_load32(s_col + 32 * c, x);
-            tmem_wait_ld();
+            uint32_t see = column_mask(first, last, 32 * c);
+            if ((gone >> (2 * c)) & 1u) see &= 0xFFFF0000u;
+            if ((gone >> (2 * c)) & 2u) see &= 0x0000FFFFu;
 #pragma unroll
-            for (int k = 0; k < 32; ++k) {
-              const int col = 32 * c + k;
-              if (col <= last && col >= first && !((gone >> (col >> 4)) & 1u)) mx = fmaxf(mx, __uint_as_float(x[k]) * c2);
-            }
+            for (int k = 0; k < 32; ++k)
+              if (!((see >> k) & 1u)) x[32 * c + k] = -CUDART_INF_F;
           }
-          const float un = fminf(up, kShift - mx);
+        }
+        float mx[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mx[k] = fmax3(x[k], x[k + 4], x[k + 8]);
+#pragma unroll
+        for (int k = 12; k < 124; k += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mx[e] = fmax3(mx[e], x[k + e], x[k + 4 + e]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], x[124 + e]);
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c2;
+        if (__any_sync(0xffffffffu, top + up > kShift + kLag)) {
+          // a new maximum: the first tile's, or one that has grown by kLag
+          const float un = fminf(up, kShift - top);
           const float a = ex2(un - up);
           up = un;
           l *= a;
           if (t > ta[i]) {                              // the products before are complete: S_i of this tile came after them
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t x[32];
-              tmem_load32(o_col + 32 * c, x);
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t o[16];
+              tmem_load16(o_col + 16 * c, o);
               tmem_wait_ld();
 #pragma unroll
-              for (int k = 0; k < 32; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * a);
-              tmem_store32(o_col + 32 * c, x);
+              for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * a);
+              tmem_store16(o_col + 16 * c, o);
             }
           }
         }
+        const uint64_t c22 = pack_f32x2(c2, c2), up2 = pack_f32x2(up, up);
+        uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
         for (int c = 0; c < kChTile / 32; ++c) {
-          uint32_t x[32], w[16];
-          tmem_load32(s_col + 32 * c, x);
-          tmem_wait_ld();
-#pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            float y = __fmaf_rn(__uint_as_float(x[k]), c2, up);
-            if (masked) {
-              const int col = 32 * c + k;
-              if (!(col <= last && col >= first && !((gone >> (col >> 4)) & 1u))) y = -CUDART_INF_F;
-            }
-            x[k] = __float_as_uint(ex2(y));
-          }
+          uint32_t w[16];
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
-            l += __uint_as_float(x[2 * k]) + __uint_as_float(x[2 * k + 1]);
-            w[k] = pack_f16x2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1]));
+            const uint64_t y = ffma2(pack_f32x2(x[32 * c + 2 * k], x[32 * c + 2 * k + 1]), c22, up2);
+            const float e0 = ex2(lo_f32(y)), e1 = ex2(hi_f32(y));
+            sum[k & 1] = fadd2(sum[k & 1], pack_f32x2(e0, e1));
+            w[k] = pack_f16x2(e0, e1);
           }
-          tmem_store16(s_col + 16 * c, w);              // over columns of S that have been read
+          tmem_store16(s_col + 16 * c, w);              // over S, which is in registers
         }
+        sum[0] = fadd2(sum[0], sum[1]);
+        l += lo_f32(sum[0]) + hi_f32(sum[0]);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -374,6 +408,7 @@ __global__ void __launch_bounds__(kChThreads, 1) attention_chunk_kernel(AttnArgs
       }
     } else if (warp < kChConvWarp + kChConvWarps) {
       // -------------------------------------------- conversion, a token each
+      regs_shrink<kChConvRegs>();
       const int r = threadIdx.x - 32 * kChConvWarp;     // token of the tile
       const int n = u.t1 - u.t0;
       auto lookup = [&](int t) -> uint32_t {
@@ -437,8 +472,10 @@ __global__ void __launch_bounds__(kChThreads, 1) attention_chunk_kernel(AttnArgs
         row = next;
         next = after;
       }
-    } else if (lane == 0) {
+    } else {
       // ----------------------------------------------------------------- MMA
+      regs_shrink<kChMmaRegs>();
+      if (warp == kChMmaWarp && lane == 0) {
       constexpr uint32_t kIdQK = idesc_f16(kChTile, false), kIdPV = idesc_f16(D, true);
       const int n = u.t1 - u.t0;
       bool ok = ch_wait(q_full, 0, abort_flag);
@@ -489,6 +526,7 @@ __global__ void __launch_bounds__(kChThreads, 1) attention_chunk_kernel(AttnArgs
       // what was issued completes before the tensor memory is given back
       tc_commit(drain);
       ch_wait(drain, 0, nullptr, kChDrainNs);
+      }
     }
   }
   __syncwarp();
