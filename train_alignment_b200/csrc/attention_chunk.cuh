@@ -7,17 +7,18 @@
 //   warps 8..11   convert a tile's E2M1 codes and E4M3 scales to FP16 (exact:
 //                 at most 6 significant bits) in shared memory, a token per
 //                 thread, keys and values in the same 128-byte-swizzled rows;
-//   warp 12       issues S_i = Q_i K^T and O_i += P_i V (tcgen05, FP16
+//   warp 12       issues S = Q_i K^T and O_i += P_i V (tcgen05, FP16
 //                 operands, FP32 accumulators in tensor memory; V is read as
 //                 the matrix whose reduction runs over its rows);
-//   warps 0..3, 4..7  own tile 0 and 1, a row per thread: the maximum of S_i,
-//                 then exp(S_i - m) as FP16 over S_i's own columns (the A
-//                 operand of the second product), the row's sum in FP32.
-// The two tiles alternate, so one's products run during the other's
-// exponentials.  O_i is rescaled only when a row's maximum has grown by more
-// than 2^kLag since the last time.
-// Tensor memory: S_0, S_1 at columns 0 and 128 (P_i in the first 64 of them),
-// O_0, O_1 at 256 and 384.
+//   warps 0..3, 4..7  own tile 0 and 1, a row per thread: S goes to registers
+//                 at once, so that one S serves both tiles; then its maximum,
+//                 and exp(S - m) as FP16 to P_i (the A operand of the second
+//                 product), the row's sum in FP32.
+// Q_i K^T of the next keys runs during the exponentials of these, and the
+// products of one tile during the other's.  O_i is rescaled only when a row's
+// maximum has grown by more than 2^kLag since the last time.
+// Tensor memory: S at column 0, P_0 and P_1 at 128 and 192, O_0 and O_1 at 256
+// and 384.
 //
 // Where the rows give fewer CTAs than SMs the keys are split too, and
 // attention_join_kernel joins the parts.  Every wait is bounded.
@@ -37,7 +38,7 @@ constexpr int kChThreads = 512;                  // four warpgroups of 128 regis
 constexpr int kChSoftRegs = 192, kChConvRegs = 88, kChMmaRegs = 40;
 static_assert(2 * kChSoftRegs + kChConvRegs + kChMmaRegs <= 4 * 128, "registers of the four warpgroups");
 constexpr int kChStages = 2;
-constexpr uint32_t kChOCol = 256;
+constexpr uint32_t kChPCol = 128, kChOCol = 256;   // P_i at kChPCol + 64 i, O_i at kChOCol + 128 i
 constexpr uint64_t kChTimeoutNs = 4000000000ull, kChDrainNs = 500000000ull;
 __host__ __device__ constexpr int ch_tile_bytes(int D) { return kChTile * D * 2; }
 __host__ __device__ constexpr int ch_smem_bytes(int D) { return 1024 + (2 + 2 * kChStages) * ch_tile_bytes(D) + 256; }
@@ -84,6 +85,17 @@ __device__ __forceinline__ void tmem_store32(uint32_t taddr, const uint32_t (&r)
       : "memory");
 }
 
+// ch_wait by a whole warp that goes on together.
+__device__ __forceinline__ bool ch_wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  return __all_sync(0xffffffffu, ch_wait(bar, parity, abort_flag));
+}
+
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+  return one != 0;
+}
 template <int kRegs>
 __device__ __forceinline__ void regs_grow() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
@@ -154,14 +166,15 @@ __global__ void __launch_bounds__(kChThreads, 1) attention_chunk_kernel(AttnArgs
   auto v_empty = [&](int s) { return bar0 + 64 + 8u * s; };
   auto s_full = [&](int i) { return bar0 + 80 + 8u * i; };
   auto p_full = [&](int i) { return bar0 + 96 + 8u * i; };
-  auto o_full = [&](int i) { return bar0 + 112 + 8u * i; };
-  uint8_t* const misc = base_ptr + (bar0 + 128 - base);
+  auto pv_done = [&](int i) { return bar0 + 112 + 8u * i; };
+  const uint32_t s_free = bar0 + 128;
+  uint8_t* const misc = base_ptr + (bar0 + 136 - base);
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(misc);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(misc + 4);
   volatile uint32_t* const gone_s = reinterpret_cast<volatile uint32_t*>(misc + 8);   // [8]: groups of 16 keys without a page
   int* const unit_s = reinterpret_cast<int*>(misc + 40);                             // {sequence, block}
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // uniform
   // the block'th 256 rows, counted through the sequences
   const int block = static_cast<int>(blockIdx.x) / p.c.n_heads;
   if (warp == 0) {
@@ -202,8 +215,9 @@ __global__ void __launch_bounds__(kChThreads, 1) attention_chunk_kernel(AttnArgs
       mbar_init(v_empty(i), 1);
       mbar_init(s_full(i), 1);
       mbar_init(p_full(i), kChSoftWarps / 2);
-      mbar_init(o_full(i), 1);
+      mbar_init(pv_done(i), 1);
     }
+    mbar_init(s_free, kChSoftWarps / 2);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -214,7 +228,7 @@ __global__ void __launch_bounds__(kChThreads, 1) attention_chunk_kernel(AttnArgs
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
   const int b = unit_s[0];
   if (b >= 0) {
@@ -278,7 +292,7 @@ __global__ void __launch_bounds__(kChThreads, 1) attention_chunk_kernel(AttnArgs
       if (lane == 0) mbar_arrive(q_full);
 
       const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-      const uint32_t s_col = tmem + lane_base + i * kChTile, o_col = tmem + lane_base + kChOCol + i * kChTile;
+      const uint32_t s_col = tmem + lane_base, p_col = s_col + kChPCol + 64 * i, o_col = s_col + kChOCol + kChTile * i;
       const int pos = u.s.pos0 + tok;
       float up = kShift - kNoMax, l = 0.0f;
       bool ok = true;
@@ -299,6 +313,9 @@ __global__ void __launch_bounds__(kChThreads, 1) attention_chunk_kernel(AttnArgs
         tmem_load32_at<64>(s_col + 64, x);
         tmem_load32_at<96>(s_col + 96, x);
         tmem_wait_ld();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(s_free);
         if (masked) {
 #pragma unroll
           for (int c = 0; c < kChTile / 32; ++c) {
@@ -326,7 +343,10 @@ __global__ void __launch_bounds__(kChThreads, 1) attention_chunk_kernel(AttnArgs
           const float a = ex2(un - up);
           up = un;
           l *= a;
-          if (t > ta[i]) {                              // the products before are complete: S_i of this tile came after them
+          if (t > ta[i]) {
+            ok = __all_sync(0xffffffffu, ch_wait(pv_done(i), (t - 1 - ta[i]) & 1, abort_flag));
+            if (!ok) break;
+            tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < D / 16; ++c) {
               uint32_t o[16];
@@ -337,6 +357,11 @@ __global__ void __launch_bounds__(kChThreads, 1) attention_chunk_kernel(AttnArgs
               tmem_store16(o_col + 16 * c, o);
             }
           }
+        }
+        if (t > ta[i]) {                                // P_i has been read
+          ok = __all_sync(0xffffffffu, ch_wait(pv_done(i), (t - 1 - ta[i]) & 1, abort_flag));
+          if (!ok) break;
+          tc_fence_after();
         }
         const uint64_t c22 = pack_f32x2(c2, c2), up2 = pack_f32x2(up, up);
         uint64_t sum[2] = {0ull, 0ull};
@@ -350,7 +375,7 @@ __global__ void __launch_bounds__(kChThreads, 1) attention_chunk_kernel(AttnArgs
             sum[k & 1] = fadd2(sum[k & 1], pack_f32x2(e0, e1));
             w[k] = pack_f16x2(e0, e1);
           }
-          tmem_store16(s_col + 16 * c, w);              // over S, which is in registers
+          tmem_store16(p_col + 16 * c, w);
         }
         sum[0] = fadd2(sum[0], sum[1]);
         l += lo_f32(sum[0]) + hi_f32(sum[0]);
@@ -359,7 +384,7 @@ __global__ void __launch_bounds__(kChThreads, 1) attention_chunk_kernel(AttnArgs
         __syncwarp();
         if (lane == 0) mbar_arrive(p_full(i));
       }
-      if (ok && tb[i] > ta[i]) ok = __all_sync(0xffffffffu, ch_wait(o_full(i), 0, abort_flag));
+      if (ok && tb[i] > ta[i]) ok = __all_sync(0xffffffffu, ch_wait(pv_done(i), (tb[i] - 1 - ta[i]) & 1, abort_flag));
       if (ok && (i == 0 || two)) {
         tc_fence_after();
         const bool some = tb[i] > ta[i];
@@ -475,57 +500,67 @@ __global__ void __launch_bounds__(kChThreads, 1) attention_chunk_kernel(AttnArgs
     } else {
       // ----------------------------------------------------------------- MMA
       regs_shrink<kChMmaRegs>();
-      if (warp == kChMmaWarp && lane == 0) {
-      constexpr uint32_t kIdQK = idesc_f16(kChTile, false), kIdPV = idesc_f16(D, true);
-      const int n = u.t1 - u.t0;
-      bool ok = ch_wait(q_full, 0, abort_flag);
-      auto active = [&](int i, int t) { return u.t0 + t >= ta[i] && u.t0 + t < tb[i]; };
-      auto scores = [&](int i, int t) {                 // S_i = Q_i K^T of tile t
-        const uint32_t kt = k_s + (t % kChStages) * kTB, qt = q_s + i * kTB;
+      if (warp == kChMmaWarp) {
+        // The whole warp keeps step, and one elected lane issues: descriptors
+        // then stay in uniform registers.  (One lane alone in a branch took
+        // about 110 cycles for each product, which is more than its 64.)
+        constexpr uint32_t kIdQK = idesc_f16(kChTile, false), kIdPV = idesc_f16(D, true);
+        const int n = u.t1 - u.t0;
+        bool ok = ch_wait_warp(q_full, 0, abort_flag);
+        auto active = [&](int i, int t) { return u.t0 + t >= ta[i] && u.t0 + t < tb[i]; };
+        int used = 0;                                   // how often S has been written
+        auto scores = [&](int i, int t) {               // S = Q_i K^T of tile t, once the last S has been read
+          if (!active(i, t)) return;
+          if (used && !ch_wait_warp(s_free, (used - 1) & 1, abort_flag)) { ok = false; return; }
+          ++used;
+          tc_fence_after();
+          const uint64_t qd = desc_kmajor_sw128(q_s + i * kTB), kd = desc_kmajor_sw128(k_s + (t % kChStages) * kTB);
+          if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t at = (kk >> 2) * (kChTile * 128) + (kk & 3) * 32;
-          mma_bf16(tmem + i * kChTile, desc_kmajor_sw128(qt + at), desc_kmajor_sw128(kt + at), kIdQK, kk != 0);
-        }
-        tc_commit(s_full(i));
-      };
-      if (n > 0 && ok) {
-        ok = ch_wait(k_full(0), 0, abort_flag);
-        tc_fence_after();
-        if (ok) {
-          for (int i = 0; i < 2; ++i)
-            if (active(i, 0)) scores(i, 0);
-          tc_commit(k_empty(0));
-        }
-      }
-      for (int t = 0; t < n && ok; ++t) {
-        const int st = t % kChStages;
-        const uint32_t parity = (t / kChStages) & 1;
-        ok = ch_wait(v_full(st), parity, abort_flag);
-        if (ok && t + 1 < n) ok = ch_wait(k_full((t + 1) % kChStages), ((t + 1) / kChStages) & 1, abort_flag);
-        if (!ok) break;
-        tc_fence_after();
-        for (int i = 0; i < 2 && ok; ++i) {
-          if (active(i, t)) {
-            ok = ch_wait(p_full(i), (u.t0 + t - ta[i]) & 1, abort_flag);
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t vt = v_s + st * kTB;
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t at = ((kk >> 2) * (kChTile * 128) + (kk & 3) * 32) >> 4;
+              mma_bf16(tmem, qd + at, kd + at, kIdQK, kk != 0);
+            }
+            tc_commit(s_full(i));
+          }
+          __syncwarp();
+        };
+        auto values = [&](int i, int t) {               // O_i += P_i V of tile t
+          if (!active(i, t)) return;
+          if (!ch_wait_warp(p_full(i), (u.t0 + t - ta[i]) & 1, abort_flag)) { ok = false; return; }
+          tc_fence_after();
+          const uint64_t vd = desc_rows_sw128(v_s + (t % kChStages) * kTB);
+          const uint32_t more = u.t0 + t > ta[i] ? 1u : 0u;
+          if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < kChTile / 16; ++kk)
-              mma_bf16_tmem_a(tmem + kChOCol + i * kChTile, tmem + i * kChTile + 8 * kk, desc_rows_sw128(vt + kk * 2048), kIdPV,
-                              (u.t0 + t > ta[i] || kk != 0) ? 1u : 0u);
-            if (u.t0 + t + 1 == tb[i]) tc_commit(o_full(i));
+              mma_bf16_tmem_a(tmem + kChOCol + i * kChTile, tmem + kChPCol + 64 * i + 8 * kk, vd + kk * (2048 >> 4), kIdPV,
+                              kk != 0 ? 1u : more);
+            tc_commit(pv_done(i));
           }
-          if (t + 1 < n && active(i, t + 1)) scores(i, t + 1);
+          __syncwarp();
+        };
+        auto release = [&](uint32_t bar) {
+          if (elect_one()) tc_commit(bar);
+          __syncwarp();
+        };
+        for (int t = 0; t <= n && ok; ++t) {            // scores of tile t, values of tile t - 1
+          if (t < n) ok = ch_wait_warp(k_full(t % kChStages), (t / kChStages) & 1, abort_flag);
+          if (ok && t < n) scores(0, t);
+          if (ok && t > 0) ok = ch_wait_warp(v_full((t - 1) % kChStages), ((t - 1) / kChStages) & 1, abort_flag);
+          if (ok && t > 0) values(0, t - 1);
+          if (ok && t < n) {
+            scores(1, t);
+            release(k_empty(t % kChStages));
+          }
+          if (ok && t > 0) {
+            values(1, t - 1);
+            release(v_empty((t - 1) % kChStages));
+          }
         }
-        if (!ok) break;
-        tc_commit(v_empty(st));
-        if (t + 1 < n) tc_commit(k_empty((t + 1) % kChStages));
-      }
-      // what was issued completes before the tensor memory is given back
-      tc_commit(drain);
-      ch_wait(drain, 0, nullptr, kChDrainNs);
+        // what was issued completes before the tensor memory is given back
+        release(drain);
+        ch_wait(drain, 0, nullptr, kChDrainNs);
       }
     }
   }
