@@ -640,7 +640,7 @@ int quads_kv_cache_write(const quads_kv_cache* cache, const uint16_t* k, const u
  * rollout's values): row row_off[b] + i of k_out and v_out [rows][n_heads][D]
  * is position start[b] + i of sequence b (start NULL: 0), e2m1 * e4m3 * g as
  * FP32 or rounded to BF16 (out_dtype), zeros where there is no page.  Rows of
- * no sequence are untouched.  Either output may be NULL. */
+ * no sequence are untouched.  Either output may be NULL; 32-byte aligned. */
 int quads_kv_cache_read(const quads_kv_cache* cache, const int32_t* row_off, const int32_t* start,
                         const int32_t* block_table, int n_seqs, int max_pages, int64_t rows, void* k_out,
                         void* v_out, int out_dtype, quads_stream_t stream);

@@ -32,15 +32,25 @@ size_t dec_workspace(int D, int nt) {
   return static_cast<size_t>(dec_grid(nt)) * (2 * (8 * nt) * (D * sizeof(float) + sizeof(float2)) + sizeof(int4));
 }
 
+// One CTA per unit where no context is longer than kDecWhole tiles.
+bool dec_whole(const quads_kv_cache* c, int max_pages) {
+  return static_cast<int64_t>(max_pages) * c->page_size <= kDecWhole * kDecTile;
+}
+
 template <int D, int NT>
-int launch_decode(AttnArgs p, void* ws, int unit_rows, cudaStream_t stream) {
+int launch_decode(AttnArgs p, void* ws, int unit_rows, bool whole, cudaStream_t stream) {
   const int grid = dec_grid(NT);
   const int64_t units = static_cast<int64_t>(p.c.n_seqs) * p.c.n_heads;
+  if (whole) {
+    attention_decode_kernel<D, NT, true><<<static_cast<unsigned>(units < grid ? units : grid), kDecThreads, 0, stream>>>(p, 0);
+    count_launches(1);
+    return check_launch("attention_decode_kernel");
+  }
   p.cuts = static_cast<int4*>(ws);
   p.part_o = reinterpret_cast<float*>(p.cuts + grid);
   p.part_ml = reinterpret_cast<float2*>(p.part_o + static_cast<size_t>(2) * grid * (8 * NT) * D);
   p.by_unit = units <= grid;
-  attention_decode_kernel<D, NT><<<grid, kDecThreads, 0, stream>>>(p, kDecMinQuota);
+  attention_decode_kernel<D, NT, false><<<grid, kDecThreads, 0, stream>>>(p, kDecMinQuota);
   QUADS_TRY(check_launch("attention_decode_kernel"));
   // the joining kernel is resident before the last run ends and waits for it
   cudaLaunchAttribute attr{};
@@ -113,7 +123,7 @@ size_t quads_attention_paged_workspace_bytes(const quads_kv_cache* cache, int64_
   if (cache == nullptr || cache->n_heads < 1 || heads_q < 1 || heads_q % cache->n_heads != 0) return 0;
   if (rows <= 0 || n_seqs <= 0 || max_q_len <= 0 || max_pages < 0) return 0;
   const int64_t unit_rows = static_cast<int64_t>(max_q_len) * (heads_q / cache->n_heads);
-  if (unit_rows <= 16) return dec_workspace(cache->head_dim, unit_rows <= 8 ? 1 : 2);
+  if (unit_rows <= 16) return dec_whole(cache, max_pages) ? 0 : dec_workspace(cache->head_dim, unit_rows <= 8 ? 1 : 2);
   return chunk_workspace(cache, rows, heads_q, chunk_plan(cache, rows, heads_q, n_seqs, max_pages, max_q_len).n_split);
 }
 
@@ -151,9 +161,10 @@ int quads_attention_paged(const uint16_t* q, int64_t rows, int64_t ld_q, int hea
     QUADS_REQUIRE(tiles < (int64_t(1) << 30) && tiles * n_seqs * cache->n_heads < (int64_t(1) << 30),
                   QUADS_ERR_UNSUPPORTED_SHAPE, "n_seqs * n_heads * max_pages * page_size must be below 2^36");
     const int n = static_cast<int>(unit_rows);
+    const bool whole = dec_whole(cache, max_pages);
     if (cache->head_dim == 64)
-      return n <= 8 ? launch_decode<64, 1>(p, ws, n, stream) : launch_decode<64, 2>(p, ws, n, stream);
-    return n <= 8 ? launch_decode<128, 1>(p, ws, n, stream) : launch_decode<128, 2>(p, ws, n, stream);
+      return n <= 8 ? launch_decode<64, 1>(p, ws, n, whole, stream) : launch_decode<64, 2>(p, ws, n, whole, stream);
+    return n <= 8 ? launch_decode<128, 1>(p, ws, n, whole, stream) : launch_decode<128, 2>(p, ws, n, whole, stream);
   }
   const ChunkPlan plan = chunk_plan(cache, rows, heads_q, n_seqs, max_pages, max_q_len);
   QUADS_REQUIRE(plan.blocks * cache->n_heads < (int64_t(1) << 31) && ceil_div(rows * heads_q, int64_t(8)) < (int64_t(1) << 31),

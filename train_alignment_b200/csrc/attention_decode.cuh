@@ -6,6 +6,9 @@
 // sequences of any lengths load the SMs alike.  A unit that spans several
 // CTAs leaves partial sums that attention_combine_kernel joins in order.
 //
+// Where no context is longer than kDecWhole tiles, a CTA takes whole units and
+// nothing is joined.
+//
 // A CTA's four warps take 16 keys each of a tile, straight from global memory
 // into the registers of the matrix instructions (m16n8k16, keys as M: the
 // rows of up to 8 (16) queries are its N, so a group of 8 query heads wastes
@@ -28,6 +31,7 @@ namespace quads {
 constexpr int kDecThreads = 128;
 constexpr int kDecWarps = kDecThreads / 32;
 constexpr int kDecTile = 16 * kDecWarps;
+constexpr int kDecWhole = 16;
 // resident CTAs of an SM: its registers hold 96 (160) a thread
 __host__ __device__ constexpr int dec_ctas_per_sm(int nt) { return nt == 1 ? 4 : 3; }
 constexpr int kMaxRuns = 1024;      // CTAs of a launch
@@ -210,7 +214,7 @@ struct DecRaw {
   }
 };
 
-template <int D, int NT>
+template <int D, int NT, bool kWhole>
 __global__ void __launch_bounds__(kDecThreads, dec_ctas_per_sm(NT)) attention_decode_kernel(AttnArgs p, int min_quota) {
   constexpr int kRows = 8 * NT;
   constexpr int kMT = D / 16;                           // 16-element tiles of O^T
@@ -225,25 +229,44 @@ __global__ void __launch_bounds__(kDecThreads, dec_ctas_per_sm(NT)) attention_de
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
-  int quota, w0, w1;
+  // a run of tiles [w0, w1), or (kWhole) units blockIdx.x, + gridDim.x, ...
+  int quota = 1, w0 = blockIdx.x, w1 = p.c.n_seqs * p.c.n_heads, b = 0, base = 0;
   bool told = false;                                    // thread 0: this run's cut is written
-  if (!plan.run(p, min_quota, quota, w0, w1)) {
-    if (!p.by_unit && threadIdx.x == 0) p.cuts[blockIdx.x] = make_int4(-1, 0, 0, 0);
-    return;
+  if constexpr (!kWhole) {
+    if (!plan.run(p, min_quota, quota, w0, w1)) {
+      if (!p.by_unit && threadIdx.x == 0) p.cuts[blockIdx.x] = make_int4(-1, 0, 0, 0);
+      return;
+    }
+    b = plan.b;
+    base = plan.base;
   }
-  int b = plan.b, base = plan.base;
 
   for (int w = w0; w < w1;) {
-    SeqInfo s = plan.info(p, b);
-    int nt = dec_tiles(s);
-    while (w >= base + nt * p.c.n_heads) {              // on to the next sequence with rows
-      base += nt * p.c.n_heads;
-      s = plan.info(p, ++b);
+    SeqInfo s;
+    int nt, head, tile0, tile1;
+    if constexpr (kWhole) {
+      b = static_cast<int>(static_cast<unsigned>(w) / static_cast<unsigned>(p.c.n_heads));
+      head = w - b * p.c.n_heads;
+      s = seq_info(p, b);
       nt = dec_tiles(s);
+      tile0 = 0;
+      tile1 = nt;
+      if (nt == 0) {
+        w += gridDim.x;
+        continue;
+      }
+    } else {
+      s = plan.info(p, b);
+      nt = dec_tiles(s);
+      while (w >= base + nt * p.c.n_heads) {            // on to the next sequence with rows
+        base += nt * p.c.n_heads;
+        s = plan.info(p, ++b);
+        nt = dec_tiles(s);
+      }
+      head = static_cast<int>(static_cast<unsigned>(w - base) / static_cast<unsigned>(nt));
+      tile0 = w - base - head * nt;
+      tile1 = min(nt, tile0 + (w1 - w));
     }
-    const int head = static_cast<int>(static_cast<unsigned>(w - base) / static_cast<unsigned>(nt));
-    const int tile0 = w - base - head * nt;
-    const int tile1 = min(nt, tile0 + (w1 - w));
     const int R = min(s.nq * p.group, kRows);
 
     // queries: lane (g, t) holds elements [t D / 4, (t + 1) D / 4) of row g of each group of 8
@@ -471,9 +494,9 @@ __global__ void __launch_bounds__(kDecThreads, dec_ctas_per_sm(NT)) attention_de
       }
     __syncthreads();
     const int slot = 2 * blockIdx.x + (w == w0 ? 0 : 1);
-    const bool whole = tile0 == 0 && tile1 == nt;
+    const bool whole = kWhole || (tile0 == 0 && tile1 == nt);
     // the run that begins a unit says whether and where others go on with it
-    if (tile0 == 0 && threadIdx.x == 0) {
+    if (!kWhole && tile0 == 0 && threadIdx.x == 0) {
       const int last = static_cast<int>(static_cast<unsigned>(w + nt - 1) / static_cast<unsigned>(quota));
       const int4 cut = make_int4(whole ? -1 : slot, last, s.r0 * p.c.n_heads + head, R);
       if (p.by_unit)
@@ -525,9 +548,9 @@ __global__ void __launch_bounds__(kDecThreads, dec_ctas_per_sm(NT)) attention_de
       }
     }
     __syncthreads();
-    w += tile1 - tile0;
+    w += kWhole ? static_cast<int>(gridDim.x) : tile1 - tile0;
   }
-  if (!p.by_unit && threadIdx.x == 0 && !told) p.cuts[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  if (!kWhole && !p.by_unit && threadIdx.x == 0 && !told) p.cuts[blockIdx.x] = make_int4(-1, 0, 0, 0);
 }
 
 // Joins the partial sums of a unit that several runs share: block (x, y) takes

@@ -86,12 +86,46 @@ __device__ __forceinline__ void locate_rows(const CacheArgs& c, const int32_t* _
   __syncthreads();
 }
 
+// 32-byte global accesses.
+__device__ __forceinline__ void load_32b(const void* p, uint32_t (&w)[8]) {
+  asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+               : "l"(p));
+}
+__device__ __forceinline__ void store_32b(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
+// The blocks of 16 elements of a row: sides (keys, values) x heads x D / 16.
+struct BlockMap {
+  FastDiv row_div;             // by the blocks of a row
+  int per_side, nb_log2, nb_mask;
+};
+struct Block {
+  int r, head, blk;
+  bool second;                 // of the second side
+};
+__device__ __forceinline__ Block block_of(const BlockMap& m, int i) {
+  Block b;
+  b.r = static_cast<int>(fast_div(static_cast<uint32_t>(i), m.row_div));
+  int j = i - b.r * static_cast<int>(m.row_div.d);
+  b.second = j >= m.per_side;
+  if (b.second) j -= m.per_side;
+  b.head = j >> m.nb_log2;
+  b.blk = j & m.nb_mask;
+  return b;
+}
+
 // --------------------------------------------------------------- the write
-// One thread per block of 16 elements: 32 bytes in, 8 + 1 bytes out.  Bound
-// by HBM: 2 bytes read and 0.5625 written per element.
+// One thread per block of 16 elements: 32 bytes in (one access where the rows
+// are 32-byte aligned), 8 + 1 bytes out.  Bound by HBM: 2 bytes read and
+// 0.5625 written per element.
+template <bool kWide>
 __global__ void __launch_bounds__(kThreads) kv_write_kernel(CacheArgs c, const uint16_t* __restrict__ k,
                                                             const uint16_t* __restrict__ v, int64_t rows,
-                                                            int64_t ld_k, int64_t ld_v, int D,
+                                                            int64_t ld_k, int64_t ld_v, BlockMap map,
                                                             const int32_t* __restrict__ off,
                                                             const int32_t* __restrict__ kv_len, int per_cta) {
   __shared__ int page_s[kMaxRows], at_s[kMaxRows];
@@ -99,72 +133,94 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(CacheArgs c, const u
   const int n = static_cast<int>(min(static_cast<int64_t>(per_cta), rows - r0));
   locate_rows(c, off, r0, n, page_s, at_s,
               [&](int b) { return static_cast<int64_t>(__ldg(kv_len + b)) - (__ldg(off + b + 1) - __ldg(off + b)); });
-  const int nb = D / 16, per_side = c.n_heads * nb, per_row = 2 * per_side;
-  for (int i = threadIdx.x; i < n * per_row; i += kThreads) {
-    const int r = i / per_row, j = i - r * per_row;
-    const int page = page_s[r];
+  const int nb = map.nb_mask + 1;
+  for (int i = threadIdx.x; i < n * static_cast<int>(map.row_div.d); i += kThreads) {
+    const Block x = block_of(map, i);
+    const int page = page_s[x.r];
     if (page < 0) continue;
-    const bool is_v = j >= per_side;
-    const int jj = is_v ? j - per_side : j;
-    const int head = jj / nb, blk = jj - head * nb;
-    const uint16_t* src = is_v ? v + (r0 + r) * ld_v : k + (r0 + r) * ld_k;
+    const uint16_t* src = (x.second ? v + (r0 + x.r) * ld_v : k + (r0 + x.r) * ld_k) + (x.head * nb + x.blk) * 16;
     uint32_t w[8];
-    load_bf16x16(src + jj * 16, w);
-    const QCore q = quant_core(w, __ldg((is_v ? c.g_v : c.g_k) + head));
-    const int64_t row = cache_row(c, page, head, at_s[r]);
-    *reinterpret_cast<uint2*>((is_v ? c.v_codes : c.k_codes) + row * (D / 2) + blk * 8) = make_uint2(q.lo, q.hi);
-    (is_v ? c.v_scales : c.k_scales)[row * nb + blk] = static_cast<uint8_t>(q.scale);
+    if constexpr (kWide) load_32b(src, w);
+    else load_bf16x16(src, w);
+    const QCore q = quant_core(w, __ldg((x.second ? c.g_v : c.g_k) + x.head));
+    const int64_t at = cache_row(c, page, x.head, at_s[x.r]) * nb + x.blk;
+    *reinterpret_cast<uint2*>((x.second ? c.v_codes : c.k_codes) + at * 8) = make_uint2(q.lo, q.hi);
+    (x.second ? c.v_scales : c.k_scales)[at] = static_cast<uint8_t>(q.scale);
   }
 }
 
 // ---------------------------------------------------------------- the read
-// One thread per 16 bytes of output (8 BF16 or 4 FP32 values), so that a
-// warp stores whole lines.  Bound by HBM: 0.5625 bytes read and 2 or 4
-// written per element.
+// One thread per block of 16 elements, four blocks in flight: 8 + 1 bytes in,
+// 32 (BF16) or 64 (FP32) out in 32-byte stores.  Bound by HBM: 0.5625 bytes
+// read and 2 or 4 written per element.
+constexpr int kReadUnroll = 4;
+
 template <bool kF32>
 __global__ void __launch_bounds__(kThreads) kv_read_kernel(CacheArgs c, void* __restrict__ k_out,
-                                                           void* __restrict__ v_out, int64_t rows, int D,
+                                                           void* __restrict__ v_out, int64_t rows, BlockMap map,
                                                            const int32_t* __restrict__ off,
                                                            const int32_t* __restrict__ start, int per_cta) {
-  constexpr int kVec = kF32 ? 4 : 8;
   __shared__ int page_s[kMaxRows], at_s[kMaxRows];
   const int64_t r0 = static_cast<int64_t>(blockIdx.x) * per_cta;
   const int n = static_cast<int>(min(static_cast<int64_t>(per_cta), rows - r0));
   locate_rows(c, off, r0, n, page_s, at_s, [&](int b) -> int64_t { return start != nullptr ? __ldg(start + b) : 0; });
-  const int nv = D / kVec, per_side = c.n_heads * nv;
-  const int sides = (k_out != nullptr) + (v_out != nullptr), per_row = sides * per_side;
-  for (int i = threadIdx.x; i < n * per_row; i += kThreads) {
-    const int r = i / per_row, j = i - r * per_row;
-    const int page = page_s[r];
-    if (page == -2) continue;
-    const bool is_v = k_out == nullptr || j >= per_side;
-    const int jj = j >= per_side ? j - per_side : j;
-    const int head = jj / nv, x = (jj - head * nv) * kVec;
-    uint32_t codes = 0, s = 0;
-    if (page >= 0) {
-      const int64_t row = cache_row(c, page, head, at_s[r]);
-      codes = __ldg(reinterpret_cast<const uint32_t*>((is_v ? c.v_codes : c.k_codes) + row * (D / 2) + x / 8 * 4));
-      s = __ldg((is_v ? c.v_scales : c.k_scales) + row * (D / 16) + x / 16);
-    }
-    const float g = __ldg((is_v ? c.g_v : c.g_k) + head), sv = e4m3_value(s);
-    uint32_t h[4];
-    e2m1x8_to_f16x2(codes, h);                         // 8 elements, of which FP32 takes its half
-    if (kF32 && (x & 4)) {
-      h[0] = h[2];
-      h[1] = h[3];
-    }
-    const uint64_t sv2 = pack_f32x2(sv, sv), g2 = pack_f32x2(g, g);
-    uint64_t f[4];                                     // e2m1 * e4m3 is exact, one rounding with g
+  const int nb = map.nb_mask + 1, total = n * static_cast<int>(map.row_div.d);
+  const bool one_side = k_out == nullptr;               // values alone: they are the first side
+  for (int i0 = threadIdx.x; i0 < total; i0 += kReadUnroll * kThreads) {
+    uint2 codes[kReadUnroll];
+    uint32_t s[kReadUnroll];
 #pragma unroll
-    for (int e = 0; e < kVec / 2; ++e) f[e] = fmul2_rn(fmul2_rn(f16x2_to_f32x2(h[e]), sv2), g2);
-    const int64_t o = (r0 + r) * (static_cast<int64_t>(c.n_heads) * D) + head * D + x;
-    void* const out = is_v ? v_out : k_out;
-    if constexpr (kF32)
-      *reinterpret_cast<float4*>(static_cast<float*>(out) + o) =
-          make_float4(lo_f32(f[0]), hi_f32(f[0]), lo_f32(f[1]), hi_f32(f[1]));
-    else
-      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + o) =
-          make_uint4(f32x2_to_bf16x2(f[0]), f32x2_to_bf16x2(f[1]), f32x2_to_bf16x2(f[2]), f32x2_to_bf16x2(f[3]));
+    for (int u = 0; u < kReadUnroll; ++u) {
+      const int i = i0 + u * kThreads;
+      codes[u] = make_uint2(0, 0);
+      s[u] = 0;
+      if (i < total) {
+        const Block x = block_of(map, i);
+        const int page = page_s[x.r];
+        if (page >= 0) {
+          const int64_t at = cache_row(c, page, x.head, at_s[x.r]) * nb + x.blk;
+          const bool is_v = one_side || x.second;
+          codes[u] = __ldg(reinterpret_cast<const uint2*>((is_v ? c.v_codes : c.k_codes) + at * 8));
+          s[u] = __ldg((is_v ? c.v_scales : c.k_scales) + at);
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kReadUnroll; ++u) {
+      const int i = i0 + u * kThreads;
+      if (i >= total) break;
+      const Block x = block_of(map, i);
+      if (page_s[x.r] == -2) continue;
+      const bool is_v = one_side || x.second;
+      const float g = __ldg((is_v ? c.g_v : c.g_k) + x.head), sv = e4m3_value(s[u]);
+      const uint64_t sv2 = pack_f32x2(sv, sv), g2 = pack_f32x2(g, g);
+      uint32_t h[2][4];
+      e2m1x8_to_f16x2(codes[u].x, h[0]);
+      e2m1x8_to_f16x2(codes[u].y, h[1]);
+      uint64_t f[8];                                   // e2m1 * e4m3 is exact, one rounding with g
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = fmul2_rn(fmul2_rn(f16x2_to_f32x2(h[e >> 2][e & 3]), sv2), g2);
+      const int64_t o = ((r0 + x.r) * c.n_heads + x.head) * (16 * nb) + x.blk * 16;
+      void* const out = is_v ? v_out : k_out;
+      if constexpr (kF32) {
+        float* const d = static_cast<float*>(out) + o;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t w[8];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            w[2 * e] = static_cast<uint32_t>(f[4 * half + e]);
+            w[2 * e + 1] = static_cast<uint32_t>(f[4 * half + e] >> 32);
+          }
+          store_32b(d + 8 * half, w);
+        }
+      } else {
+        uint32_t w[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = f32x2_to_bf16x2(f[e]);
+        store_32b(static_cast<uint16_t*>(out) + o, w);
+      }
+    }
   }
 }
 
@@ -247,6 +303,11 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(RopeArgs p, int per_cta)
   }
 }
 
+BlockMap block_map(const quads_kv_cache* c, int sides) {
+  const int nb = c->head_dim / 16;                      // 4 or 8
+  return BlockMap{make_fastdiv(static_cast<uint32_t>(sides * c->n_heads * nb)), c->n_heads * nb, nb == 4 ? 2 : 3, nb - 1};
+}
+
 // Rows of a CTA: as many as keep `want` items of work, fewer where the call
 // is too small to give every SM four CTAs.
 int rows_per_cta(int64_t rows, int per_row, int want) {
@@ -278,9 +339,13 @@ int quads_kv_cache_write(const quads_kv_cache* cache, const uint16_t* k, const u
   QUADS_REQUIRE(k && v && kv_len, QUADS_ERR_INVALID_ARG, "null pointer");
   QUADS_REQUIRE(aligned(k, 16) && aligned(v, 16), QUADS_ERR_INVALID_ARG, "k and v must be 16-byte aligned");
   const CacheArgs c = cache_args(cache, block_table, n_seqs, max_pages);
-  const int per = rows_per_cta(rows, static_cast<int>(width / 8), 1024);
-  kv_write_kernel<<<static_cast<unsigned>(ceil_div(rows, int64_t(per))), kThreads, 0, stream>>>(
-      c, k, v, rows, ld_k, ld_v, cache->head_dim, row_off, kv_len, per);
+  const BlockMap map = block_map(cache, 2);
+  const int per = rows_per_cta(rows, static_cast<int>(map.row_div.d), 1024);
+  const unsigned grid = static_cast<unsigned>(ceil_div(rows, int64_t(per)));
+  if (aligned(k, 32) && aligned(v, 32) && ld_k % 16 == 0 && ld_v % 16 == 0)
+    kv_write_kernel<true><<<grid, kThreads, 0, stream>>>(c, k, v, rows, ld_k, ld_v, map, row_off, kv_len, per);
+  else
+    kv_write_kernel<false><<<grid, kThreads, 0, stream>>>(c, k, v, rows, ld_k, ld_v, map, row_off, kv_len, per);
   count_launches(1);
   return check_launch("kv_write_kernel");
 }
@@ -296,16 +361,16 @@ int quads_kv_cache_read(const quads_kv_cache* cache, const int32_t* row_off, con
                 "unknown output dtype %d", out_dtype);
   if (rows == 0 || n_seqs == 0) return QUADS_OK;
   QUADS_REQUIRE(k_out || v_out, QUADS_ERR_INVALID_ARG, "no output");
-  QUADS_REQUIRE(aligned(k_out, 16) && aligned(v_out, 16), QUADS_ERR_INVALID_ARG, "outputs must be 16-byte aligned");
+  QUADS_REQUIRE(aligned(k_out, 32) && aligned(v_out, 32), QUADS_ERR_INVALID_ARG, "outputs must be 32-byte aligned");
   const CacheArgs c = cache_args(cache, block_table, n_seqs, max_pages);
   const bool f32 = out_dtype == QUADS_OUT_F32;
-  const int per_row = cache->n_heads * cache->head_dim / (f32 ? 4 : 8) * ((k_out != nullptr) + (v_out != nullptr));
-  const int per = rows_per_cta(rows, per_row, 4096);
+  const BlockMap map = block_map(cache, (k_out != nullptr) + (v_out != nullptr));
+  const int per = rows_per_cta(rows, static_cast<int>(map.row_div.d), 2048);
   const unsigned grid = static_cast<unsigned>(ceil_div(rows, int64_t(per)));
   if (f32)
-    kv_read_kernel<true><<<grid, kThreads, 0, stream>>>(c, k_out, v_out, rows, cache->head_dim, row_off, start, per);
+    kv_read_kernel<true><<<grid, kThreads, 0, stream>>>(c, k_out, v_out, rows, map, row_off, start, per);
   else
-    kv_read_kernel<false><<<grid, kThreads, 0, stream>>>(c, k_out, v_out, rows, cache->head_dim, row_off, start, per);
+    kv_read_kernel<false><<<grid, kThreads, 0, stream>>>(c, k_out, v_out, rows, map, row_off, start, per);
   count_launches(1);
   return check_launch("kv_read_kernel");
 }
