@@ -7,6 +7,7 @@ import torch
 
 from train_alignment_b200 import attention as A
 from train_alignment_b200 import binding as B
+from train_alignment_b200 import workloads as W
 
 P = 1 << 20          # a stand-in for an aligned device address: no call below reaches the device
 
@@ -121,3 +122,10 @@ def test_rope_frequencies():
                 dict(rot_dim=64, factor=0.0), dict(rot_dim=2, scaling="base")):
         with pytest.raises(ValueError):
             A.rope_frequencies(device="cpu", **bad)
+
+
+def test_sequence_lengths():
+    for T, n in ((300, 3), (4096, 5), (7, 7), (1, 1)):
+        lens = W.sequence_lengths(T, n)
+        assert len(lens) == n and sum(lens) == T and all(x >= 0 for x in lens)
+    assert len(set(W.sequence_lengths(4096, 5))) == 5

@@ -1,4 +1,5 @@
-"""The rollout's key/value cache in NVFP4, and the frequencies of rotary positions.
+"""The rollout's key/value cache in NVFP4, rotary frequencies, and a layer's
+attention over the cache on both sides of RL alignment.
 
 [TRACE] "Le problème", "Résultats": the rollout keeps weights, activations
 and the KV cache in FP4.  KVCache holds the pages and their decode scales; it
@@ -11,6 +12,7 @@ import math
 import torch
 
 from . import binding as B
+from . import workloads as W
 
 
 class KVCache:
@@ -80,3 +82,75 @@ def rope_frequencies(rot_dim, theta=10000.0, scaling=None, factor=1.0, original_
     elif scaling not in (None, "base"):
         raise ValueError(f"unknown scaling {scaling!r}")
     return freq.to(device)
+
+
+class CachedAttention:
+    """One layer's attention: BF16 projections (library matmuls), rotary
+    positions, the paged NVFP4 cache and the attention over it.
+
+    Rollout: keys and values are quantized into the cache as they are written
+    and the new tokens attend over it.  Trainer: in a recorded layer its own
+    queries attend over the rollout's cache, the values the rollout used
+    ([TRACE] "Fonctionnement": the trainer reproduces them); elsewhere it
+    quantizes its own keys and values on the same grid, with the rollout's
+    decode scales, into a cache of its own.
+    """
+
+    def __init__(self, acfg: W.AttnConfig, w_qkv, w_o, lengths, device="cuda"):
+        self.cfg, self.w_qkv, self.w_o = acfg, w_qkv, w_o
+        self.dev = torch.device(device)
+        self.lengths = [int(n) for n in lengths]
+        self.T, self.longest = sum(self.lengths), max(self.lengths)
+        pages = [-(-n // acfg.page) for n in self.lengths]
+        self.n_pages, width = sum(pages), max(pages)
+        i32 = lambda a: torch.tensor(a, dtype=torch.int32, device=self.dev)
+        first = [sum(pages[:b]) for b in range(len(pages))]
+        self.table = i32([[first[b] + j if j < pages[b] else -1 for j in range(width)] for b in range(len(pages))])
+        self.off = i32([sum(self.lengths[:b]) for b in range(len(pages) + 1)])
+        self.kv_len = i32(self.lengths)
+        self.pos = torch.cat([torch.arange(n, device=self.dev) for n in self.lengths])
+        self.freq = rope_frequencies(acfg.rot, acfg.theta, device=self.dev)
+        self.cache = self.t_cache = None
+
+    def project(self, x):
+        """Rotated queries and keys, and values, of x [T, H]: [T, heads, dim] each."""
+        c = self.cfg
+        qkv = (x @ self.w_qkv.t()).view(self.T, c.heads_q + 2 * c.heads_k, c.dim)
+        q, k = B.rope(qkv[:, :c.heads_q], qkv[:, c.heads_q:c.heads_q + c.heads_k], self.pos, self.freq,
+                      interleaved=c.interleaved)
+        return q, k, qkv[:, c.heads_q + c.heads_k:]
+
+    def calibrate(self, x):
+        """Sets each head's decode scales from x and allocates both sides' caches."""
+        _, k, v = self.project(x)
+        amax = [t.abs().amax(dim=(0, 2)).float() for t in (k, v)]
+        c = self.cfg
+        self.cache, self.t_cache = (KVCache.empty(self.n_pages, c.page, c.heads_k, c.dim, *amax, device=self.dev)
+                                    for _ in range(2))
+
+    def attend(self, q, cache):
+        o = B.attention_paged(q, cache, self.off, self.kv_len, self.table, self.longest, window=self.cfg.window)
+        return o.view(self.T, -1) @ self.w_o.t()
+
+    def rollout(self, x):
+        """The attention's output [T, H]; leaves keys and values in the cache."""
+        q, k, v = self.project(x)
+        B.kv_cache_write(self.cache, k, v, self.off, self.kv_len, self.table)
+        return self.attend(q, self.cache)
+
+    def trainer(self, x, replay):
+        """The trainer's output [T, H]: over the rollout's cache (replay), or
+        over its own keys and values on the same grid."""
+        q, k, v = self.project(x)
+        if replay:
+            return self.attend(q, self.cache)
+        B.kv_cache_write(self.t_cache, k, v, self.off, self.kv_len, self.table)
+        return self.attend(q, self.t_cache)
+
+    def kv_gap(self, x):
+        """Relative distances of the trainer's own keys and values of x from
+        those that the rollout cached, read back (a reported diagnostic)."""
+        _, k, v = self.project(x)
+        kr, vr = B.kv_cache_read(self.cache, self.off, self.table, self.T, out_dtype=B.OUT_F32)
+        rel = lambda a, b: float(torch.linalg.vector_norm(a.float() - b) / torch.linalg.vector_norm(b).clamp_min(1e-30))
+        return rel(k, kr), rel(v, vr)

@@ -8,6 +8,13 @@ Rollout side: every layer runs the NVFP4 path (MoELayer) and the last
 `recorded` layers export their TRACE record (codes, scales, per-tensor
 scales, residuals, top-k indices) [TRACE "L'idée centrale"].
 
+With an AttnConfig every layer has attention before its MoE, over an NVFP4
+key/value cache ([TRACE] "Résultats": FP4 weights, activations and KV cache):
+x_{l+1/2} = x_l + Attn_l(x_l), x_{l+1} = x_{l+1/2} + MoE_l(x_{l+1/2}).  In the
+recorded layers the trainer's queries attend over the rollout's cache; in the
+others (and in the W4A4 ablation) the trainer quantizes its own keys and
+values.  Without one (the default) the stack is the MoE layers alone.
+
 Trainer side ([QUADS-fr §2.2.A]): BF16 activations with the fake-quantized
 weights W_fq.  In the recorded layers the trainer replays the record
 [TRACE "L'idée centrale", "Fonctionnement"]:
@@ -37,14 +44,17 @@ down GEMM and the combine.
 """
 import torch
 
+from . import attention as A
 from . import binding as B
 from . import layer as L
 from . import workloads as W
 
 
 class LayerStack:
-    def __init__(self, cfg: W.MoEConfig, seed=0, device="cuda", recorded=4, trainer_gemm="w4a16"):
+    def __init__(self, cfg: W.MoEConfig, seed=0, device="cuda", recorded=4, trainer_gemm="w4a16",
+                 attn: W.AttnConfig = None):
         self.cfg = cfg
+        self.attn = None
         self.dev = torch.device(device)
         self.recorded = min(recorded, cfg.layers)
         if trainer_gemm not in ("w4a16", "library"):
@@ -57,10 +67,21 @@ class LayerStack:
         # build layer by layer: each layer's channel sets are calibrated on the
         # activations that actually reach it
         self.layers = []
+        if attn is not None:
+            self.attn = []
+            lengths = W.sequence_lengths(T, attn.n_seqs)
+            self.x_mid = torch.empty(cfg.layers, T, H, dtype=torch.bfloat16, device=self.dev)     # rollout MoE inputs
+            self.x_mid_train = torch.empty_like(self.x_mid)
         x = self.x0.clone()
         logits = torch.empty(T, E, dtype=torch.float32, device=self.dev)
         for l in range(cfg.layers):
             inp = inp0 if l == 0 else W.moe_layer_inputs(cfg, seed, device, layer=l, with_logits=False)
+            if attn is not None:
+                w = W.attention_weights(cfg, attn, seed, device, layer=l)
+                a = A.CachedAttention(attn, w["w_qkv"], w["w_o"], lengths, device)
+                a.calibrate(x)
+                x = B.residual_add(x, a.rollout(x))
+                self.attn.append(a)
             B.router_logits(x, self.w_r[l], out=logits)
             layer = L.build_layer(cfg, {"x": x, "logits": logits, "w_gu": inp["w_gu"], "w_d": inp["w_d"]}, device)
             layer.weight_sync()
@@ -91,12 +112,15 @@ class LayerStack:
         the stack output in x_roll[L]."""
         self.x_roll[0].copy_(x0)
         for l, layer in enumerate(self.layers):
-            B.router_logits(self.x_roll[l], self.w_r[l], out=self.logits)
+            x = self.x_roll[l]
+            if self.attn is not None:
+                x = B.residual_add(x, self.attn[l].rollout(x), out=self.x_mid[l])
+            B.router_logits(x, self.w_r[l], out=self.logits)
             layer.weight_sync()
-            out = layer.rollout_forward(self.x_roll[l], self.logits)
+            out = layer.rollout_forward(x, self.logits)
             if self.is_recorded(l):
                 layer.export(l)
-            B.residual_add(self.x_roll[l], out, out=self.x_roll[l + 1])
+            B.residual_add(x, out, out=self.x_roll[l + 1])
         return self.x_roll[self.cfg.layers]
 
     def _trainer_ffn(self, layer, x, idx, w, w4a4=False):
@@ -173,6 +197,9 @@ class LayerStack:
         code_mis = scale_mis = 0
         for l, layer in enumerate(self.layers):
             xl = self.x_train[l]
+            if self.attn is not None:
+                o = self.attn[l].trainer(xl, replay=self.is_recorded(l) and not w4a4)
+                xl = B.residual_add(xl, o, out=self.x_mid_train[l])
             if self.is_recorded(l) and not w4a4:
                 layer.reset_counts()
                 layer.trainer_replay(xl, layer_id=l)
@@ -202,3 +229,9 @@ class LayerStack:
         a, b = y_r.float(), y_t.float()
         gap = torch.linalg.vector_norm(a - b, dim=1) / torch.linalg.vector_norm(b, dim=1).clamp_min(1e-30)
         return gap, cm, sm
+
+    def kv_gaps(self):
+        """Per recorded layer of a stack with attention, after an alignment
+        pass: (key, value) distances of the trainer's own from the rollout's
+        cached ones."""
+        return {l: a.kv_gap(self.x_train[l]) for l, a in enumerate(self.attn or []) if self.is_recorded(l)}

@@ -52,6 +52,24 @@ class LinearConfig:
     description: str = ""
 
 
+@dataclass(frozen=True)
+class AttnConfig:
+    """Attention between the MoE layers of a stack: query and key heads, their
+    size, the rotated part of it, the cache's page, and how many sequences the
+    stack's tokens form."""
+    heads_q: int
+    heads_k: int
+    dim: int
+    rot: int
+    page: int = 64
+    n_seqs: int = 1
+    theta: float = 10000.0
+    interleaved: bool = False
+    window: int = 0
+
+
+ATTN_H2048 = AttnConfig(heads_q=16, heads_k=4, dim=128, rot=128, page=64, n_seqs=5)
+
 LINEAR_64x256x512 = LinearConfig(
     "linear_m64_k256_n512", 64, 256, 512, 8, 4, 20.0,
     "single NVFP4 linear: X 64x256 N(0,1) with 4 outlier channels x20, "
@@ -183,6 +201,21 @@ def stack_router_weights(cfg: MoEConfig, seed=0, device="cpu"):
     gen = _gen(device, seed * 7919 + 424242)
     return (torch.randn(cfg.layers, cfg.H, cfg.E, generator=gen, device=device)
             / math.sqrt(cfg.H)).contiguous()
+
+
+def attention_weights(cfg: MoEConfig, acfg: AttnConfig, seed=0, device="cpu", layer=0):
+    """Projections of one layer's attention, BF16 ~ N(0, 0.02): w_qkv [(heads_q +
+    2 heads_k) dim, H] (queries, keys, values), w_o [H, heads_q dim]."""
+    gen = _gen(device, seed * 7919 + layer * 1000 + 161803)
+    d = acfg.dim
+    return {"w_qkv": _randn_bf16(((acfg.heads_q + 2 * acfg.heads_k) * d, cfg.H), 0.02, gen, device),
+            "w_o": _randn_bf16((cfg.H, acfg.heads_q * d), 0.02, gen, device)}
+
+
+def sequence_lengths(T, n):
+    """T tokens as n sequences of different lengths (the i-th about twice i's share)."""
+    cuts = [T * i * (i + 1) // (n * (n + 1)) for i in range(n + 1)]
+    return [b - a for a, b in zip(cuts, cuts[1:])]
 
 
 def engine_drift(x, std, seed, device="cpu"):
