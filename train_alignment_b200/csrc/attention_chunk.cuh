@@ -297,7 +297,7 @@ __global__ void __launch_bounds__(kChThreads, 1) attention_chunk_kernel(AttnArgs
       float up = kShift - kNoMax, l = 0.0f;
       bool ok = true;
       for (int t = ta[i]; t < tb[i]; ++t) {
-        ok = __all_sync(0xffffffffu, ch_wait(s_full(i), (t - ta[i]) & 1, abort_flag));
+        ok = ch_wait_warp(s_full(i), (t - ta[i]) & 1, abort_flag);
         if (!ok) break;
         tc_fence_after();
         const int j0 = u.s.lo + t * kChTile;
@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(kChThreads, 1) attention_chunk_kernel(AttnArgs
           up = un;
           l *= a;
           if (t > ta[i]) {
-            ok = __all_sync(0xffffffffu, ch_wait(pv_done(i), (t - 1 - ta[i]) & 1, abort_flag));
+            ok = ch_wait_warp(pv_done(i), (t - 1 - ta[i]) & 1, abort_flag);
             if (!ok) break;
             tc_fence_after();
 #pragma unroll 1
@@ -358,25 +358,25 @@ __global__ void __launch_bounds__(kChThreads, 1) attention_chunk_kernel(AttnArgs
             }
           }
         }
-        if (t > ta[i]) {                                // P_i has been read
-          ok = __all_sync(0xffffffffu, ch_wait(pv_done(i), (t - 1 - ta[i]) & 1, abort_flag));
-          if (!ok) break;
-          tc_fence_after();
-        }
         const uint64_t c22 = pack_f32x2(c2, c2), up2 = pack_f32x2(up, up);
         uint64_t sum[2] = {0ull, 0ull};
+        uint32_t w[kChTile / 32][16];
 #pragma unroll
-        for (int c = 0; c < kChTile / 32; ++c) {
-          uint32_t w[16];
+        for (int c = 0; c < kChTile / 32; ++c)
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
             const uint64_t y = ffma2(pack_f32x2(x[32 * c + 2 * k], x[32 * c + 2 * k + 1]), c22, up2);
             const float e0 = ex2(lo_f32(y)), e1 = ex2(hi_f32(y));
             sum[k & 1] = fadd2(sum[k & 1], pack_f32x2(e0, e1));
-            w[k] = pack_f16x2(e0, e1);
+            w[c][k] = pack_f16x2(e0, e1);
           }
-          tmem_store16(p_col + 16 * c, w);
+        if (t > ta[i]) {                                // P_i has been read
+          ok = ch_wait_warp(pv_done(i), (t - 1 - ta[i]) & 1, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
         }
+#pragma unroll
+        for (int c = 0; c < kChTile / 32; ++c) tmem_store16(p_col + 16 * c, w[c]);
         sum[0] = fadd2(sum[0], sum[1]);
         l += lo_f32(sum[0]) + hi_f32(sum[0]);
         tmem_wait_st();
@@ -384,7 +384,7 @@ __global__ void __launch_bounds__(kChThreads, 1) attention_chunk_kernel(AttnArgs
         __syncwarp();
         if (lane == 0) mbar_arrive(p_full(i));
       }
-      if (ok && tb[i] > ta[i]) ok = __all_sync(0xffffffffu, ch_wait(pv_done(i), (tb[i] - 1 - ta[i]) & 1, abort_flag));
+      if (ok && tb[i] > ta[i]) ok = ch_wait_warp(pv_done(i), (tb[i] - 1 - ta[i]) & 1, abort_flag);
       if (ok && (i == 0 || two)) {
         tc_fence_after();
         const bool some = tb[i] > ta[i];
@@ -480,7 +480,7 @@ __global__ void __launch_bounds__(kChThreads, 1) attention_chunk_kernel(AttnArgs
       for (int t = 0; t < n; ++t) {
         const int st = t % kChStages;
         const uint32_t free_parity = ((t / kChStages) & 1) ^ 1u;
-        if (!__all_sync(0xffffffffu, ch_wait(k_empty(st), free_parity, abort_flag))) break;
+        if (!ch_wait_warp(k_empty(st), free_parity, abort_flag)) break;
         // groups of 16 keys without a page (those past the last key are masked by position)
         const unsigned no = __ballot_sync(0xffffffffu, row == kNoRow);
         if (lane == 0)
@@ -490,7 +490,7 @@ __global__ void __launch_bounds__(kChThreads, 1) attention_chunk_kernel(AttnArgs
         if (lane == 0) mbar_arrive(k_full(st));
         const uint32_t after = lookup(t + 2);
         load(p.c.k_codes, p.c.k_scales, next, kc, ks);
-        if (!__all_sync(0xffffffffu, ch_wait(v_empty(st), free_parity, abort_flag))) break;
+        if (!ch_wait_warp(v_empty(st), free_parity, abort_flag)) break;
         convert(v_s + st * kTB, vc, vs);
         if (lane == 0) mbar_arrive(v_full(st));
         load(p.c.v_codes, p.c.v_scales, next, vc, vs);

@@ -32,7 +32,8 @@ constexpr int kDecThreads = 128;
 constexpr int kDecWarps = kDecThreads / 32;
 constexpr int kDecTile = 16 * kDecWarps;
 constexpr int kDecWhole = 16;
-// resident CTAs of an SM: its registers hold 96 (160) a thread
+// resident CTAs of an SM: its registers hold 128 (168) a thread (five of 96
+// registers spill and take 10 % longer)
 __host__ __device__ constexpr int dec_ctas_per_sm(int nt) { return nt == 1 ? 4 : 3; }
 constexpr int kMaxRuns = 1024;      // CTAs of a launch
 
@@ -184,7 +185,7 @@ struct DecRaw {
   uint32_t v[4][D / 64];
   uint32_t vs[4];
 
-  __device__ __forceinline__ void read(const uint8_t* st, int g, int t) {
+  __device__ __forceinline__ void read_keys(const uint8_t* st, int g, int t) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int key = dec_key(g) + 8 * i;
@@ -198,6 +199,8 @@ struct DecRaw {
         ks[i] = st[16 * D + key * 4 + t];
       }
     }
+  }
+  __device__ __forceinline__ void read_values(const uint8_t* st, int g, int t) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int key = dec_key(2 * t + (i & 1)) + 8 * (i >> 1);
@@ -332,7 +335,9 @@ __global__ void __launch_bounds__(kDecThreads, dec_ctas_per_sm(NT)) attention_de
     uint32_t gone_now = __ballot_sync(0xffffffffu, rows_now == kNoRow), gone_next = 0u;   // bit i: step i has no page
     if (rows_now == kNoRow) rows_now = 0u;
 
-    auto attend = [&](const DecRaw<D>& x, int j0, bool gone) {
+    auto attend = [&](const uint8_t* st, int j0, bool gone) {
+      DecRaw<D> x;
+      x.read_keys(st, g, t);
       // S^T = K Q^T
       float sc[NT][4];
 #pragma unroll
@@ -412,6 +417,7 @@ __global__ void __launch_bounds__(kDecThreads, dec_ctas_per_sm(NT)) attention_de
         pb[n][1] = move_trans(pack_f16x2(e2, e3));
       }
       // O^T += V^T P^T
+      x.read_values(st, g, t);
       const uint32_t sa = scale_pair_f16x2(x.vs[0], x.vs[1]), sb = scale_pair_f16x2(x.vs[2], x.vs[3]);
 #pragma unroll
       for (int j = 0; j < D / 64; ++j) {
@@ -468,9 +474,7 @@ __global__ void __launch_bounds__(kDecThreads, dec_ctas_per_sm(NT)) attention_de
         if (ahead < steps) copy.load(row, ring_a + (u + kDecStages - 1) % kDecStages * kStage, lane);
         cp_async_commit();
         if (u == 0 && (step & 31) == 0) gone_cur = gone_now;      // ahead has passed into this step's 32
-        DecRaw<D> x;
-        x.read(ring + u * kStage, g, t);
-        attend(x, j_first + step * kDecTile, (gone_cur >> (step & 31)) & 1u);
+        attend(ring + u * kStage, j_first + step * kDecTile, (gone_cur >> (step & 31)) & 1u);
       }
     }
     cp_async_wait<0>();
