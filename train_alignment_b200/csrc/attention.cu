@@ -20,6 +20,23 @@ int attention_wait_status(unsigned int* v) {
 
 namespace {
 
+// Launches a kernel that may become resident before the one in front of it in
+// the stream has ended, and waits for that itself.
+template <typename... Params, typename... Args>
+int launch_dependent(void (*kernel)(Params...), dim3 grid, int threads, cudaStream_t stream, const char* what, Args... args) {
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) return check_launch(what);
+  return QUADS_OK;
+}
+
 // CTAs of the kernel for few rows: as many as are resident at once.
 int dec_grid(int nt) {
   const int n = dec_ctas_per_sm(nt) * num_sms();
@@ -52,19 +69,9 @@ int launch_decode(AttnArgs p, void* ws, int unit_rows, bool whole, cudaStream_t 
   p.by_unit = units <= grid;
   attention_decode_kernel<D, NT, false><<<grid, kDecThreads, 0, stream>>>(p, kDecMinQuota);
   QUADS_TRY(check_launch("attention_decode_kernel"));
-  // the joining kernel is resident before the last run ends and waits for it
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
   // rows on blocks of their own where few units are cut into many runs
-  cfg.gridDim = dim3(static_cast<unsigned>(p.by_unit ? units : grid), units * 8 <= grid ? unit_rows : 1);
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.stream = stream;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, attention_combine_kernel<D, NT>, p) != cudaSuccess)
-    return check_launch("attention_combine_kernel");
+  const dim3 join(static_cast<unsigned>(p.by_unit ? units : grid), units * 8 <= grid ? unit_rows : 1);
+  QUADS_TRY(launch_dependent(attention_combine_kernel<D, NT>, join, kJoinThreads, stream, "attention_combine_kernel", p));
   count_launches(2);
   return QUADS_OK;
 }
@@ -105,10 +112,11 @@ int launch_chunk(AttnArgs p, const ChunkPlan& plan, void* ws, cudaStream_t strea
   count_launches(1);
   QUADS_TRY(check_launch("attention_chunk_kernel"));
   if (plan.n_split > 1) {
-    attention_join_kernel<D><<<static_cast<unsigned>(ceil_div(p.rows * p.hq, int64_t(8))), 256, 0, stream>>>(p, plan.n_split);
+    const dim3 join(static_cast<unsigned>(ceil_div(p.rows * p.hq, int64_t(8))));
+    QUADS_TRY(launch_dependent(attention_join_kernel<D>, join, 256, stream, "attention_join_kernel", p, plan.n_split));
     count_launches(1);
   }
-  return check_launch("attention_join_kernel");
+  return QUADS_OK;
 }
 
 }  // namespace

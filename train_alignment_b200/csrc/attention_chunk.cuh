@@ -154,6 +154,7 @@ __device__ __forceinline__ void ch_range(const AttnArgs& p, const SeqInfo& s, in
 template <int D>
 __global__ void __launch_bounds__(kChThreads, 1) attention_chunk_kernel(AttnArgs p, int n_split) {
   extern __shared__ uint8_t smem_raw[];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t raw = smem_addr(smem_raw), base = (raw + 1023u) & ~1023u;
   uint8_t* const base_ptr = smem_raw + (base - raw);
   constexpr int kTB = ch_tile_bytes(D);
@@ -571,37 +572,63 @@ __global__ void __launch_bounds__(kChThreads, 1) attention_chunk_kernel(AttnArgs
   if (warp == kChMmaWarp) tmem_dealloc(tmem, 512);
 }
 
-// Joins the parts of rows whose keys were split: one warp per (row, head).
+// Joins the parts of rows whose keys were split: one warp per (row, head), the
+// parts' weights a lane each.
 template <int D>
 __global__ void __launch_bounds__(256) attention_join_kernel(AttnArgs p, int n_split) {
   const int lane = threadIdx.x & 31;
   const int64_t item = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
   const int64_t r = item / p.hq;
-  if (r >= p.rows) return;
   const int h = static_cast<int>(item - r * p.hq);
-  const int b = warp_find_seq(p.off, p.c.n_seqs, static_cast<int>(r), lane);
-  if (b < 0) return;
-  const SeqInfo s = seq_info(p, b);
-  if (r >= s.r0 + s.nq) return;
+  bool mine = false;
+  if (r < p.rows) {
+    const int b = warp_find_seq(p.off, p.c.n_seqs, static_cast<int>(r), lane);
+    if (b >= 0) {
+      const SeqInfo s = seq_info(p, b);
+      mine = r < s.r0 + s.nq;
+    }
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");    // every block, so that this kernel ends after the first
+  if (!mine) return;
   constexpr int kE = D / 32;
-  float m = kNoMax, l = 0.0f, o[kE];
+  const int64_t at = r * p.hq + h, step = p.rows * p.hq;
+  float m = kNoMax;
+  for (int i = lane; i < n_split; i += 32) m = fmaxf(m, __ldcg(p.part_ml + at + i * step).x);
+#pragma unroll
+  for (int k = 16; k; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
+  float l = 0.0f, o[kE];
 #pragma unroll
   for (int e = 0; e < kE; ++e) o[e] = 0.0f;
-  for (int i = 0; i < n_split; ++i) {
-    const int64_t at = (static_cast<int64_t>(i) * p.rows + r) * p.hq + h;
-    const float2 ml = __ldcg(p.part_ml + at);
-    if (ml.y <= 0.0f) continue;                         // a part without keys has no sums
-    const float mn = fmaxf(m, ml.x), a = ex2(m - mn), f = ex2(ml.x - mn);
-    m = mn;
-    l = l * a + ml.y * f;
+  for (int i0 = 0; i0 < n_split; i0 += 32) {
+    float f = 0.0f;
+    if (i0 + lane < n_split) {
+      const float2 ml = __ldcg(p.part_ml + at + (i0 + lane) * step);
+      f = ml.y > 0.0f ? ex2(ml.x - m) : 0.0f;           // a part without keys has no sums
+      l += ml.y * f;
+    }
+    const int n = min(32, n_split - i0);
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const float w = __shfl_sync(0xffffffffu, f, i);
+      float y[kE];
+      if constexpr (kE == 4) {
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(p.part_o + (at + (i0 + i) * step) * D) + lane);
+        y[0] = v.x; y[1] = v.y; y[2] = v.z; y[3] = v.w;
+      } else {
+        const float2 v = __ldcg(reinterpret_cast<const float2*>(p.part_o + (at + (i0 + i) * step) * D) + lane);
+        y[0] = v.x; y[1] = v.y;
+      }
 #pragma unroll
-    for (int e = 0; e < kE; ++e) o[e] = o[e] * a + __ldcg(p.part_o + at * D + lane * kE + e) * f;
+      for (int e = 0; e < kE; ++e) o[e] = w > 0.0f ? __fmaf_rn(y[e], w, o[e]) : o[e];
+    }
   }
+#pragma unroll
+  for (int k = 16; k; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
   const float inv = l > 0.0f ? kScaleUnit * __ldg(p.c.g_v + h / p.group) / l : 0.0f;
-  uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + (r * p.hq + h) * D + lane * kE);
+  uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + at * D + lane * kE);
 #pragma unroll
   for (int e = 0; e < kE / 2; ++e) dst[e] = pack_bf16x2(o[2 * e] * inv, o[2 * e + 1] * inv);
-  if (lane == 0 && p.lse != nullptr) p.lse[r * p.hq + h] = l > 0.0f ? (m - kShift) * kLn2 + logf(l) : -CUDART_INF_F;
+  if (lane == 0 && p.lse != nullptr) p.lse[at] = l > 0.0f ? (m - kShift) * kLn2 + logf(l) : -CUDART_INF_F;
 }
 
 }  // namespace quads
