@@ -272,6 +272,33 @@ __global__ void __launch_bounds__(kDecThreads, dec_ctas_per_sm(NT)) attention_de
     }
     const int R = min(s.nq * p.group, kRows);
 
+    // The warp's steps of 16 keys, one per tile.  A step's keys share a page:
+    // lane i looks up the cache row of step i of 32, the next 32 half way
+    // through these.  A step without a page reads row 0 and masks it.
+    const int pos_last = s.pos0 + s.nq - 1;
+    const int j_first = s.lo + tile0 * kDecTile + 16 * warp;
+    const int steps = min(tile1 - tile0, (s.hi - j_first + kDecTile - 1) / kDecTile);     // those with a key below hi
+    auto lookup = [&](int step) -> uint32_t {
+      if (step >= steps) return 0u;
+      int at;
+      const int page = page_of(p.c, b, j_first + step * kDecTile, at);
+      return page >= 0 ? static_cast<uint32_t>(cache_row(p.c, page, head, at)) : kNoRow;
+    };
+    uint32_t rows_now = lookup(lane), rows_next = 0u;
+    uint32_t gone_now = __ballot_sync(0xffffffffu, rows_now == kNoRow), gone_next = 0u;   // bit i: step i has no page
+    if (rows_now == kNoRow) rows_now = 0u;
+
+    // one step being computed, kDecStages - 1 on their way
+    const uint8_t* const ring = buf_s + warp * (kDecStages * kStage);
+    const uint32_t ring_a = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
+    const DecCopy<D> copy(p.c, lane);
+#pragma unroll
+    for (int i = 0; i < kDecStages - 1; ++i) {
+      const uint32_t row = __shfl_sync(0xffffffffu, rows_now, i);
+      if (i < steps) copy.load(row, ring_a + i * kStage, lane);
+      cp_async_commit();
+    }
+
     // queries: lane (g, t) holds elements [t D / 4, (t + 1) D / 4) of row g of each group of 8
     uint32_t qf[NT][D / 8];
     float c2[NT][2];                                    // score factor (to powers of two) of rows 2t, 2t + 1
@@ -318,22 +345,6 @@ __global__ void __launch_bounds__(kDecThreads, dec_ctas_per_sm(NT)) attention_de
       up[n][0] = up[n][1] = kShift - kNoMax;
       l[n][0] = l[n][1] = 0.0f;
     }
-
-    // The warp's steps of 16 keys, one per tile.  A step's keys share a page:
-    // lane i looks up the cache row of step i of 32, the next 32 half way
-    // through these.  A step without a page reads row 0 and masks it.
-    const int pos_last = s.pos0 + s.nq - 1;
-    const int j_first = s.lo + tile0 * kDecTile + 16 * warp;
-    const int steps = min(tile1 - tile0, (s.hi - j_first + kDecTile - 1) / kDecTile);     // those with a key below hi
-    auto lookup = [&](int step) -> uint32_t {
-      if (step >= steps) return 0u;
-      int at;
-      const int page = page_of(p.c, b, j_first + step * kDecTile, at);
-      return page >= 0 ? static_cast<uint32_t>(cache_row(p.c, page, head, at)) : kNoRow;
-    };
-    uint32_t rows_now = lookup(lane), rows_next = 0u;
-    uint32_t gone_now = __ballot_sync(0xffffffffu, rows_now == kNoRow), gone_next = 0u;   // bit i: step i has no page
-    if (rows_now == kNoRow) rows_now = 0u;
 
     auto attend = [&](const uint8_t* st, int j0, bool gone) {
       DecRaw<D> x;
@@ -440,16 +451,6 @@ __global__ void __launch_bounds__(kDecThreads, dec_ctas_per_sm(NT)) attention_de
       }
     };
 
-    // one step being computed, kDecStages - 1 on their way
-    const uint8_t* const ring = buf_s + warp * (kDecStages * kStage);
-    const uint32_t ring_a = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
-    const DecCopy<D> copy(p.c, lane);
-#pragma unroll
-    for (int i = 0; i < kDecStages - 1; ++i) {
-      const uint32_t row = __shfl_sync(0xffffffffu, rows_now, i);
-      if (i < steps) copy.load(row, ring_a + i * kStage, lane);
-      cp_async_commit();
-    }
     uint32_t gone_cur = gone_now;
     for (int step0 = 0; step0 < steps; step0 += kDecStages) {
 #pragma unroll
