@@ -21,15 +21,24 @@ class KVCache:
     Wraps the given tensors; KVCache.empty allocates them."""
 
     def __init__(self, k_codes, k_scales, v_codes, v_scales, g_k, g_v):
-        n_pages, n_heads, page_size, half = codes = k_codes.shape
-        scales, heads, dev = (n_pages, n_heads, page_size, half // 8), (n_heads,), k_codes.get_device()
+        codes, dev = k_codes.shape, k_codes.get_device()
+        n_pages, n_heads, page_size, half = codes
+        scales, heads = (n_pages, n_heads, page_size, half // 8), (n_heads,)
         u8, f32 = torch.uint8, torch.float32
-        for t, dt, shape, name in ((k_codes, u8, codes, "k_codes"), (v_codes, u8, codes, "v_codes"),
-                                   (k_scales, u8, scales, "k_scales"), (v_scales, u8, scales, "v_scales"),
-                                   (g_k, f32, heads, "g_k"), (g_v, f32, heads, "g_v")):
-            if t.dtype is not dt or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
-                raise ValueError(f"{name} must be a contiguous {dt} tensor of shape {tuple(shape)} on {k_codes.device}, "
-                                 f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+        # written out: a cache may be wrapped around its tensors once per step
+        if not (k_codes.dtype is u8 and v_codes.dtype is u8 and k_scales.dtype is u8 and v_scales.dtype is u8
+                and g_k.dtype is f32 and g_v.dtype is f32
+                and v_codes.shape == codes and k_scales.shape == scales and v_scales.shape == scales
+                and g_k.shape == heads and g_v.shape == heads
+                and v_codes.get_device() == dev and k_scales.get_device() == dev and v_scales.get_device() == dev
+                and g_k.get_device() == dev and g_v.get_device() == dev
+                and k_codes.is_contiguous() and v_codes.is_contiguous() and k_scales.is_contiguous()
+                and v_scales.is_contiguous() and g_k.is_contiguous() and g_v.is_contiguous()):
+            got = ", ".join(f"{n} {t.dtype} {tuple(t.shape)} on {t.device}" for n, t in (
+                ("k_codes", k_codes), ("k_scales", k_scales), ("v_codes", v_codes), ("v_scales", v_scales),
+                ("g_k", g_k), ("g_v", g_v)))
+            raise ValueError(f"a cache needs contiguous uint8 codes {tuple(codes)}, uint8 scales {scales} and float32 "
+                             f"decode scales {heads} on one device, got {got}")
         self.n_pages, self.n_heads, self.page_size, self.head_dim = n_pages, n_heads, page_size, 2 * half
         self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
         self.g_k, self.g_v = g_k, g_v

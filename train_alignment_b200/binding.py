@@ -700,9 +700,9 @@ def _stream(t, name):
     """Raw current stream of t's device, which must be the current one (the
     device the launches go to)."""
     d = t.get_device()
-    if d < 0:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if d != torch.cuda.current_device():
+    if d < 0 or d != torch.cuda.current_device():
+        if d < 0:
+            raise ValueError(f"{name} must be a CUDA tensor")
         raise ValueError(f"{name} is on cuda:{d}, not on the current device cuda:{torch.cuda.current_device()}")
     return torch._C._cuda_getCurrentRawStream(d)
 
@@ -719,10 +719,9 @@ def _like(t, first, dtype, shape, name):
 def _heads_view(x, first, name):
     """A BF16 tensor [rows, heads, dim] on the device of `first` whose rows may
     be strided: (rows, heads, dim, row stride)."""
-    if x.dtype is not torch.bfloat16 or x.dim() != 3:
-        raise ValueError(f"{name} must be a bfloat16 tensor [rows, heads, dim]")
-    if x.get_device() != first.get_device():
-        raise ValueError(f"{name} is on {x.device}, not on {first.device}")
+    if x.dtype is not torch.bfloat16 or x.dim() != 3 or x.get_device() != first.get_device():
+        raise ValueError(f"{name} must be a bfloat16 tensor [rows, heads, dim] on {first.device}, got {x.dtype} "
+                         f"{tuple(x.shape)} on {x.device}")
     rows, heads, dim = x.shape
     ld, sh, sd = x.stride()
     if (sd != 1 and dim > 1) or (sh != dim and heads > 1):
@@ -732,12 +731,15 @@ def _heads_view(x, first, name):
 
 def _tables(cache, row_off, block_table):
     """Checks row_off and block_table: (n_seqs, max_pages, their pointers)."""
-    if block_table.dim() != 2:
-        raise ValueError("block_table must be [n_seqs, max_pages]")
-    n, m = block_table.shape
-    first = cache.k_codes
-    return n, m, _like(row_off, first, torch.int32, (n + 1,), "row_off"), _like(block_table, first, torch.int32, (n, m),
-                                                                                "block_table")
+    n, m = block_table.shape if block_table.dim() == 2 else (-1, -1)
+    dev, i32 = cache.k_codes.get_device(), torch.int32
+    if (n < 0 or block_table.dtype is not i32 or row_off.dtype is not i32 or row_off.shape != (n + 1,)
+            or not block_table.is_contiguous() or not row_off.is_contiguous()
+            or block_table.get_device() != dev or row_off.get_device() != dev):
+        raise ValueError(f"block_table must be a contiguous int32 tensor [n_seqs, max_pages] and row_off [n_seqs + 1] on "
+                         f"{cache.k_codes.device}, got {block_table.dtype} {tuple(block_table.shape)} on "
+                         f"{block_table.device} and {row_off.dtype} {tuple(row_off.shape)} on {row_off.device}")
+    return n, m, row_off.data_ptr(), block_table.data_ptr()
 
 
 def kv_cache_write(cache, k, v, row_off, kv_len, block_table):
@@ -767,11 +769,17 @@ def kv_cache_read(cache, row_off, block_table, rows, start=None, out_dtype=OUT_B
     shape = (rows, cache.n_heads, cache.head_dim)
     if k_out is None:
         k_out = first.new_empty(shape, dtype=dt)
+        pk = k_out.data_ptr()
+    else:
+        pk = _like(k_out, first, dt, shape, "k_out")
     if v_out is None:
         v_out = first.new_empty(shape, dtype=dt)
-    _check(load().quads_kv_cache_read(cache.ref, off, st, table, n, m, rows, _like(k_out, first, dt, shape, "k_out"),
-                                      _like(v_out, first, dt, shape, "v_out"), out_dtype, stream),
-           "quads_kv_cache_read")
+        pv = v_out.data_ptr()
+    else:
+        pv = _like(v_out, first, dt, shape, "v_out")
+    rc = load().quads_kv_cache_read(cache.ref, off, st, table, n, m, rows, pk, pv, out_dtype, stream)
+    if rc:
+        _check(rc, "quads_kv_cache_read")
     return k_out, v_out
 
 

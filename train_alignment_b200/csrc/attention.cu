@@ -43,6 +43,7 @@ int dec_grid(int nt) {
   return n < kMaxRuns ? n : kMaxRuns;
 }
 constexpr int kChMinTiles = 4;       // key tiles of a split: shorter ones cost more in joining than they save
+constexpr int kDecMaxRows = 32;      // rows of a sequence and key head up to which the kernel for few rows is taken
 constexpr int kDecMinQuota = 4;      // tiles of a run: shorter ones cost more in joining than they save
 
 size_t dec_workspace(int D, int nt) {
@@ -57,7 +58,8 @@ bool dec_whole(const quads_kv_cache* c, int max_pages) {
 template <int D, int NT>
 int launch_decode(AttnArgs p, void* ws, int unit_rows, bool whole, cudaStream_t stream) {
   const int grid = dec_grid(NT);
-  const int64_t units = static_cast<int64_t>(p.c.n_seqs) * p.c.n_heads;
+  p.row_groups = (unit_rows + 8 * NT - 1) / (8 * NT);
+  const int64_t units = static_cast<int64_t>(p.c.n_seqs) * p.c.n_heads * p.row_groups;
   if (whole) {
     attention_decode_kernel<D, NT, true><<<static_cast<unsigned>(units < grid ? units : grid), kDecThreads, 0, stream>>>(p, 0);
     count_launches(1);
@@ -70,7 +72,7 @@ int launch_decode(AttnArgs p, void* ws, int unit_rows, bool whole, cudaStream_t 
   attention_decode_kernel<D, NT, false><<<grid, kDecThreads, 0, stream>>>(p, kDecMinQuota);
   QUADS_TRY(check_launch("attention_decode_kernel"));
   // rows on blocks of their own where few units are cut into many runs
-  const dim3 join(static_cast<unsigned>(p.by_unit ? units : grid), units * 8 <= grid ? unit_rows : 1);
+  const dim3 join(static_cast<unsigned>(p.by_unit ? units : grid), units * 8 <= grid ? (unit_rows < 8 * NT ? unit_rows : 8 * NT) : 1);
   QUADS_TRY(launch_dependent(attention_combine_kernel<D, NT>, join, kJoinThreads, stream, "attention_combine_kernel", p));
   count_launches(2);
   return QUADS_OK;
@@ -131,7 +133,7 @@ size_t quads_attention_paged_workspace_bytes(const quads_kv_cache* cache, int64_
   if (cache == nullptr || cache->n_heads < 1 || heads_q < 1 || heads_q % cache->n_heads != 0) return 0;
   if (rows <= 0 || n_seqs <= 0 || max_q_len <= 0 || max_pages < 0) return 0;
   const int64_t unit_rows = static_cast<int64_t>(max_q_len) * (heads_q / cache->n_heads);
-  if (unit_rows <= 16) return dec_whole(cache, max_pages) ? 0 : dec_workspace(cache->head_dim, unit_rows <= 8 ? 1 : 2);
+  if (unit_rows <= kDecMaxRows) return dec_whole(cache, max_pages) ? 0 : dec_workspace(cache->head_dim, unit_rows <= 8 ? 1 : 2);
   return chunk_workspace(cache, rows, heads_q, chunk_plan(cache, rows, heads_q, n_seqs, max_pages, max_q_len).n_split);
 }
 
@@ -164,8 +166,8 @@ int quads_attention_paged(const uint16_t* q, int64_t rows, int64_t ld_q, int hea
   p.max_q = max_q_len; p.window = window < (1 << 30) ? window : (1 << 30); p.scale = scale;
   p.group_div = make_fastdiv(static_cast<uint32_t>(p.group));
   const int64_t unit_rows = static_cast<int64_t>(max_q_len) * p.group;
-  if (unit_rows <= 16) {
-    const int64_t tiles = static_cast<int64_t>(max_pages) * cache->page_size / kDecTile + 2;
+  if (unit_rows <= kDecMaxRows) {
+    const int64_t tiles = (static_cast<int64_t>(max_pages) * cache->page_size / kDecTile + 2) * ceil_div(unit_rows, int64_t(8));
     QUADS_REQUIRE(tiles < (int64_t(1) << 30) && tiles * n_seqs * cache->n_heads < (int64_t(1) << 30),
                   QUADS_ERR_UNSUPPORTED_SHAPE, "n_seqs * n_heads * max_pages * page_size must be below 2^36");
     const int n = static_cast<int>(unit_rows);

@@ -22,11 +22,12 @@ struct AttnArgs {
   // unnormalised sums, and {maximum, sum} of each row
   float* part_o;
   float2* part_ml;
-  // {slot of the first part or -1, CTA of the last, first row * n_heads + head,
-  // rows} of each unit (by_unit), or of the one that each CTA begins and does
-  // not end
+  // {slot of the first part or -1, CTA of the last, the sequence's first row *
+  // n_heads + head, rows | first of them << 8} of each unit (by_unit), or of
+  // the one that each CTA begins and does not end
   int4* cuts;
   int by_unit;
+  int row_groups;           // units of a sequence and key head, at most
 };
 
 // A sequence of a call: its rows, and the keys that they can see.

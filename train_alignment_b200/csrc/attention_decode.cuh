@@ -1,9 +1,9 @@
-// Attention of few rows (at most 16 per key head and sequence): bound by the
-// bytes of the cache.
+// Attention of few rows: bound by the bytes of the cache, or by the conversion
+// of its codes.
 //
-// A unit is (sequence, key head); its keys are cut into tiles of 64, and the
-// tiles of all units, end to end, into equal runs, one per CTA, so that
-// sequences of any lengths load the SMs alike.  A unit that spans several
+// A unit is (sequence, key head, 8 NT of its rows); its keys are cut into
+// tiles of 64, and the tiles of all units, end to end, into equal runs, one
+// per CTA, so that sequences of any lengths load the SMs alike.  A unit that spans several
 // CTAs leaves partial sums that attention_combine_kernel joins in order.
 //
 // Where no context is longer than kDecWhole tiles, a CTA takes whole units and
@@ -37,30 +37,39 @@ constexpr int kDecWhole = 16;
 __host__ __device__ constexpr int dec_ctas_per_sm(int nt) { return nt == 1 ? 4 : 3; }
 constexpr int kMaxRuns = 1024;      // CTAs of a launch
 
+// Key tiles of a sequence's units, and its units per head.
 __device__ __forceinline__ int dec_tiles(const SeqInfo& s) {
   if (s.nq <= 0) return 0;
   return max(1, (s.hi - s.lo + kDecTile - 1) / kDecTile);
+}
+template <int kRows>
+__device__ __forceinline__ int dec_groups(const AttnArgs& p, const SeqInfo& s) {
+  return (max(s.nq, 0) * p.group + kRows - 1) / kRows;
 }
 
 // The run of this CTA: tiles [w0, w1) of all units' (fewer than 2^30, checked
 // on the host), and the sequence of the first with the first tile of its first
 // unit.  Calls of up to kDecThreads sequences scan them once and keep them.
+template <int kRows>
 struct DecPlan {
   int warp_s[kDecWarps];
   int b, base;
   SeqInfo seq[kDecThreads];
 
-  // tiles (of one head) of sequences c0 .. c0 + kDecThreads - 1: this
+  // tiles (of one head's units) of sequences c0 .. c0 + kDecThreads - 1: this
   // thread's, those before it, and all
   __device__ __forceinline__ int scan(const AttnArgs& p, int c0, int& before, int& n) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, i = c0 + threadIdx.x;
     n = 0;
     if (i < p.c.n_seqs) {
       const SeqInfo s = seq_info(p, i);
-      n = dec_tiles(s);
+      const int groups = dec_groups<kRows>(p, s);
+      n = dec_tiles(s) * groups;
       seq[threadIdx.x] = s;
-      if (n == 0 && p.by_unit && blockIdx.x == 0)
-        for (int h = 0; h < p.c.n_heads; ++h) p.cuts[i * p.c.n_heads + h] = make_int4(-1, 0, 0, 0);
+      if (p.by_unit && blockIdx.x == 0)                 // units that this sequence has not
+        for (int h = 0; h < p.c.n_heads; ++h)
+          for (int k = groups; k < p.row_groups; ++k)
+            p.cuts[(i * p.c.n_heads + h) * p.row_groups + k] = make_int4(-1, 0, 0, 0);
     }
     int incl = n;
 #pragma unroll
@@ -227,13 +236,13 @@ __global__ void __launch_bounds__(kDecThreads, dec_ctas_per_sm(NT)) attention_de
   float (*const o_s)[kRows][D] = reinterpret_cast<float (*)[kRows][D]>(buf_s);
   __shared__ float2 ml_s[kDecWarps][kRows];
   __shared__ float f_s[kDecWarps][kRows];               // weight of each warp's sums; then 1 / l in [0]
-  __shared__ DecPlan plan;
+  __shared__ DecPlan<kRows> plan;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
   // a run of tiles [w0, w1), or (kWhole) units blockIdx.x, + gridDim.x, ...
-  int quota = 1, w0 = blockIdx.x, w1 = p.c.n_seqs * p.c.n_heads, b = 0, base = 0;
+  int quota = 1, w0 = blockIdx.x, w1 = p.c.n_seqs * p.c.n_heads * p.row_groups, b = 0, base = 0;
   bool told = false;                                    // thread 0: this run's cut is written
   if constexpr (!kWhole) {
     if (!plan.run(p, min_quota, quota, w0, w1)) {
@@ -246,31 +255,38 @@ __global__ void __launch_bounds__(kDecThreads, dec_ctas_per_sm(NT)) attention_de
 
   for (int w = w0; w < w1;) {
     SeqInfo s;
-    int nt, head, tile0, tile1;
+    int nt, head, grp, tile0, tile1;                    // grp: which 8 NT of the rows
     if constexpr (kWhole) {
-      b = static_cast<int>(static_cast<unsigned>(w) / static_cast<unsigned>(p.c.n_heads));
-      head = w - b * p.c.n_heads;
+      const int bh = static_cast<int>(static_cast<unsigned>(w) / static_cast<unsigned>(p.row_groups));
+      grp = w - bh * p.row_groups;
+      b = static_cast<int>(static_cast<unsigned>(bh) / static_cast<unsigned>(p.c.n_heads));
+      head = bh - b * p.c.n_heads;
       s = seq_info(p, b);
       nt = dec_tiles(s);
       tile0 = 0;
       tile1 = nt;
-      if (nt == 0) {
+      if (grp >= dec_groups<kRows>(p, s)) {
         w += gridDim.x;
         continue;
       }
     } else {
       s = plan.info(p, b);
       nt = dec_tiles(s);
-      while (w >= base + nt * p.c.n_heads) {            // on to the next sequence with rows
-        base += nt * p.c.n_heads;
+      int per_head = nt * dec_groups<kRows>(p, s);
+      while (w >= base + per_head * p.c.n_heads) {      // on to the next sequence with rows
+        base += per_head * p.c.n_heads;
         s = plan.info(p, ++b);
         nt = dec_tiles(s);
+        per_head = nt * dec_groups<kRows>(p, s);
       }
-      head = static_cast<int>(static_cast<unsigned>(w - base) / static_cast<unsigned>(nt));
-      tile0 = w - base - head * nt;
+      head = static_cast<int>(static_cast<unsigned>(w - base) / static_cast<unsigned>(per_head));
+      const int rest = w - base - head * per_head;
+      grp = static_cast<int>(static_cast<unsigned>(rest) / static_cast<unsigned>(nt));
+      tile0 = rest - grp * nt;
       tile1 = min(nt, tile0 + (w1 - w));
     }
-    const int R = min(s.nq * p.group, kRows);
+    const int first_row = grp * kRows;
+    const int R = min(s.nq * p.group - first_row, kRows);
 
     // The warp's steps of 16 keys, one per tile.  A step's keys share a page:
     // lane i looks up the cache row of step i of 32, the next 32 half way
@@ -309,9 +325,9 @@ __global__ void __launch_bounds__(kDecThreads, dec_ctas_per_sm(NT)) attention_de
         const int r = 8 * n + g;
         uint32_t mx = 0;
         if (r < R) {
-          const int tok = static_cast<int>(fast_div(r, p.group_div));
+          const int tok = static_cast<int>(fast_div(first_row + r, p.group_div));
           const uint4* src = reinterpret_cast<const uint4*>(
-              p.q + (s.r0 + tok) * p.ld_q + (head * p.group + (r - tok * p.group)) * D + t * (D / 4));
+              p.q + (s.r0 + tok) * p.ld_q + (head * p.group + (first_row + r - tok * p.group)) * D + t * (D / 4));
 #pragma unroll
           for (int i = 0; i < D / 32; ++i) {
             const uint4 x = __ldg(src + i);
@@ -383,7 +399,7 @@ __global__ void __launch_bounds__(kDecThreads, dec_ctas_per_sm(NT)) attention_de
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int j = j0 + dec_key(g) + 8 * (i >> 1);
-            const int pos = s.pos0 + static_cast<int>(fast_div(8 * n + 2 * t + (i & 1), p.group_div));
+            const int pos = s.pos0 + static_cast<int>(fast_div(first_row + 8 * n + 2 * t + (i & 1), p.group_div));
             const bool see = !gone && j <= pos && j < s.hi && (p.window <= 0 || j > pos - p.window);
             if (!see) y[n][i] = -CUDART_INF_F;
           }
@@ -503,9 +519,9 @@ __global__ void __launch_bounds__(kDecThreads, dec_ctas_per_sm(NT)) attention_de
     // the run that begins a unit says whether and where others go on with it
     if (!kWhole && tile0 == 0 && threadIdx.x == 0) {
       const int last = static_cast<int>(static_cast<unsigned>(w + nt - 1) / static_cast<unsigned>(quota));
-      const int4 cut = make_int4(whole ? -1 : slot, last, s.r0 * p.c.n_heads + head, R);
+      const int4 cut = make_int4(whole ? -1 : slot, last, s.r0 * p.c.n_heads + head, R | (first_row << 8));
       if (p.by_unit)
-        p.cuts[b * p.c.n_heads + head] = cut;
+        p.cuts[(b * p.c.n_heads + head) * p.row_groups + grp] = cut;
       else if (!whole)
         p.cuts[blockIdx.x] = cut;
       told |= !whole;
@@ -526,8 +542,8 @@ __global__ void __launch_bounds__(kDecThreads, dec_ctas_per_sm(NT)) attention_de
 #pragma unroll
         for (int i = 0; i < kDecWarps; ++i) f_s[i][r] *= inv;
         if (p.lse != nullptr) {
-          const int tok = static_cast<int>(fast_div(r, p.group_div));
-          p.lse[static_cast<int64_t>(s.r0 + tok) * p.hq + head * p.group + (r - tok * p.group)] =
+          const int tok = static_cast<int>(fast_div(first_row + r, p.group_div));
+          p.lse[static_cast<int64_t>(s.r0 + tok) * p.hq + head * p.group + (first_row + r - tok * p.group)] =
               ll > 0.0f ? (mm - kShift) * kLn2 + logf(ll) : -CUDART_INF_F;
         }
       } else {
@@ -545,8 +561,8 @@ __global__ void __launch_bounds__(kDecThreads, dec_ctas_per_sm(NT)) attention_de
         x.x += y.x * f; x.y += y.y * f; x.z += y.z * f; x.w += y.w * f;
       }
       if (whole) {
-        const int tok = static_cast<int>(fast_div(r, p.group_div));
-        const int64_t at = (static_cast<int64_t>(s.r0 + tok) * p.hq + head * p.group + (r - tok * p.group)) * D;
+        const int tok = static_cast<int>(fast_div(first_row + r, p.group_div));
+        const int64_t at = (static_cast<int64_t>(s.r0 + tok) * p.hq + head * p.group + (first_row + r - tok * p.group)) * D;
         reinterpret_cast<uint2*>(p.out + at)[d] = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
       } else {
         reinterpret_cast<float4*>(p.part_o + (static_cast<int64_t>(slot) * kRows + r) * D)[d] = x;
@@ -573,7 +589,7 @@ __global__ void __launch_bounds__(kJoinThreads) attention_combine_kernel(AttnArg
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int4 cut = __ldcg(p.cuts + blockIdx.x);          // slot of the first part, last run, place, rows
   if (cut.x < 0) return;
-  const int c0 = cut.x >> 1, n = cut.y - c0 + 1, R = cut.w;
+  const int c0 = cut.x >> 1, n = cut.y - c0 + 1, R = cut.w & 255, first_row = cut.w >> 8;
   const int r0 = cut.z / p.c.n_heads, head = cut.z - r0 * p.c.n_heads;
   const int grp = threadIdx.x / D, d = threadIdx.x - grp * D;
   const bool shared = n > 8;
@@ -610,8 +626,8 @@ __global__ void __launch_bounds__(kJoinThreads) attention_combine_kernel(AttnArg
       }
     }
     if (r < R && (!shared || grp == 0)) {
-      const int tok = static_cast<int>(fast_div(r, p.group_div));
-      const int64_t row = static_cast<int64_t>(r0 + tok) * p.hq + head * p.group + (r - tok * p.group);
+      const int tok = static_cast<int>(fast_div(first_row + r, p.group_div));
+      const int64_t row = static_cast<int64_t>(r0 + tok) * p.hq + head * p.group + (first_row + r - tok * p.group);
       const float inv = l > 0.0f ? kScaleUnit * __ldg(p.c.g_v + head) / l : 0.0f;
       p.out[row * D + d] = static_cast<uint16_t>(float_to_bf16_bits(o * inv));
       if (d == 0 && p.lse != nullptr) p.lse[row] = l > 0.0f ? (m - kShift) * kLn2 + logf(l) : -CUDART_INF_F;
