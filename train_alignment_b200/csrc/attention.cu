@@ -44,7 +44,7 @@ int dec_grid(int nt) {
 }
 constexpr int kChMinTiles = 4;       // key tiles of a split: shorter ones cost more in joining than they save
 constexpr int kDecMaxRows = 32;      // rows of a sequence and key head up to which the kernel for few rows is taken
-constexpr int kDecMinQuota = 4;      // tiles of a run: shorter ones cost more in joining than they save
+constexpr int kDecMinQuota = 2;      // tiles of a run: shorter ones cost more in joining than they save
 
 size_t dec_workspace(int D, int nt) {
   return static_cast<size_t>(dec_grid(nt)) * (2 * (8 * nt) * (D * sizeof(float) + sizeof(float2)) + sizeof(int4));

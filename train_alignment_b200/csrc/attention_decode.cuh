@@ -30,11 +30,12 @@ namespace quads {
 
 constexpr int kDecThreads = 128;
 constexpr int kDecWarps = kDecThreads / 32;
-constexpr int kDecTile = 16 * kDecWarps;
-constexpr int kDecWhole = 16;
+constexpr int kDecSub = 2;                            // groups of 16 keys of a warp's step
+constexpr int kDecTile = 16 * kDecSub * kDecWarps;
+constexpr int kDecWhole = 8;
 // resident CTAs of an SM: its registers hold 128 (168) a thread (five of 96
 // registers spill and take 10 % longer)
-__host__ __device__ constexpr int dec_ctas_per_sm(int nt) { return nt == 1 ? 4 : 3; }
+__host__ __device__ constexpr int dec_ctas_per_sm(int nt) { return nt == 1 ? 3 : 2; }
 constexpr int kMaxRuns = 1024;      // CTAs of a launch
 
 // Key tiles of a sequence's units, and its units per head.
@@ -142,8 +143,7 @@ __device__ __forceinline__ uint32_t move_trans(uint32_t x) {
 // value's codes is at c ^ (key / 2 % 4) (D = 128), and key i of a matrix of
 // eight is row i ^ (i / 2 % 2) of the step: both matrix operands are then read
 // without bank conflicts.
-constexpr int kDecStages = 4;
-static_assert(kDecStages == 4, "the look-up's turns (16 and 32 steps) are met at u == 1");
+constexpr int kDecStages = 2;
 __host__ __device__ constexpr int dec_stage_bytes(int D) { return 16 * (D + D / 8); }
 __device__ __forceinline__ int dec_key(int i) { return i ^ ((i >> 1) & 1); }
 
@@ -230,7 +230,7 @@ template <int D, int NT, bool kWhole>
 __global__ void __launch_bounds__(kDecThreads, dec_ctas_per_sm(NT)) attention_decode_kernel(AttnArgs p, int min_quota) {
   constexpr int kRows = 8 * NT;
   constexpr int kMT = D / 16;                           // 16-element tiles of O^T
-  constexpr int kStage = dec_stage_bytes(D), kRing = kDecWarps * kDecStages * kStage;
+  constexpr int kGroup = dec_stage_bytes(D), kStage = kDecSub * kGroup, kRing = kDecWarps * kDecStages * kStage;
   constexpr int kJoin = kDecWarps * kRows * D * 4;
   __shared__ __align__(128) uint8_t buf_s[kRing > kJoin ? kRing : kJoin];    // the warps' rings, then their sums
   float (*const o_s)[kRows][D] = reinterpret_cast<float (*)[kRows][D]>(buf_s);
@@ -292,28 +292,32 @@ __global__ void __launch_bounds__(kDecThreads, dec_ctas_per_sm(NT)) attention_de
     // lane i looks up the cache row of step i of 32, the next 32 half way
     // through these.  A step without a page reads row 0 and masks it.
     const int pos_last = s.pos0 + s.nq - 1;
-    const int j_first = s.lo + tile0 * kDecTile + 16 * warp;
+    const int j_first = s.lo + tile0 * kDecTile + 16 * kDecSub * warp;
     const int steps = min(tile1 - tile0, (s.hi - j_first + kDecTile - 1) / kDecTile);     // those with a key below hi
-    auto lookup = [&](int step) -> uint32_t {
-      if (step >= steps) return 0u;
+    auto lookup = [&](int group) -> uint32_t {
+      const int j = j_first + (group / kDecSub) * kDecTile + 16 * (group % kDecSub);
+      if (group >= kDecSub * steps || j >= s.hi) return 0u;
       int at;
-      const int page = page_of(p.c, b, j_first + step * kDecTile, at);
+      const int page = page_of(p.c, b, j, at);
       return page >= 0 ? static_cast<uint32_t>(cache_row(p.c, page, head, at)) : kNoRow;
     };
     uint32_t rows_now = lookup(lane), rows_next = 0u;
-    uint32_t gone_now = __ballot_sync(0xffffffffu, rows_now == kNoRow), gone_next = 0u;   // bit i: step i has no page
+    uint32_t gone_now = __ballot_sync(0xffffffffu, rows_now == kNoRow), gone_next = 0u;   // bit i: group i has no page
     if (rows_now == kNoRow) rows_now = 0u;
 
-    // one step being computed, kDecStages - 1 on their way
+    // one step being computed, the next on its way
     const uint8_t* const ring = buf_s + warp * (kDecStages * kStage);
     const uint32_t ring_a = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
     const DecCopy<D> copy(p.c, lane);
+    auto fetch = [&](int step, int place) {
 #pragma unroll
-    for (int i = 0; i < kDecStages - 1; ++i) {
-      const uint32_t row = __shfl_sync(0xffffffffu, rows_now, i);
-      if (i < steps) copy.load(row, ring_a + i * kStage, lane);
-      cp_async_commit();
-    }
+      for (int h = 0; h < kDecSub; ++h) {
+        const uint32_t row = __shfl_sync(0xffffffffu, rows_now, (kDecSub * step + h) & 31);
+        copy.load(row, ring_a + place * kStage + h * kGroup, lane);
+      }
+    };
+    if (steps > 0) fetch(0, 0);
+    cp_async_commit();
 
     // queries: lane (g, t) holds elements [t D / 4, (t + 1) D / 4) of row g of each group of 8
     uint32_t qf[NT][D / 8];
@@ -362,62 +366,78 @@ __global__ void __launch_bounds__(kDecThreads, dec_ctas_per_sm(NT)) attention_de
       l[n][0] = l[n][1] = 0.0f;
     }
 
-    auto attend = [&](const uint8_t* st, int j0, bool gone) {
-      DecRaw<D> x;
-      x.read_keys(st, g, t);
+    auto attend = [&](const uint8_t* st, int j0, uint32_t gone) {
+      DecRaw<D> x[kDecSub];
       // S^T = K Q^T
-      float sc[NT][4];
+      float sc[kDecSub][NT][4];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.0f;
+      for (int h = 0; h < kDecSub; ++h) {
+        x[h].read_keys(st + h * kGroup, g, t);
 #pragma unroll
-      for (int j = 0; j < D / 32; ++j) {
-        uint32_t a[4], bb[4];
-        e2m1x8_to_f16x2(x.k[0][j], a);
-        e2m1x8_to_f16x2(x.k[1][j], bb);
-        const int sh = D == 128 ? 8 * (j >> 1) : 0;
-        const uint32_t s0 = scale_f16x2(sh ? x.ks[0] >> 8 : x.ks[0] & 0xFFu), s1 = scale_f16x2(sh ? x.ks[1] >> 8 : x.ks[1] & 0xFFu);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          a[i] = hmul2_rn(a[i], s0);
-          bb[i] = hmul2_rn(bb[i], s1);
-        }
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          mma_f16(sc[n], a[0], bb[0], a[1], bb[1], qf[n][4 * j], qf[n][4 * j + 1]);
-          mma_f16(sc[n], a[2], bb[2], a[3], bb[3], qf[n][4 * j + 2], qf[n][4 * j + 3]);
-        }
+        for (int n = 0; n < NT; ++n) sc[h][n][0] = sc[h][n][1] = sc[h][n][2] = sc[h][n][3] = 0.0f;
       }
+#pragma unroll
+      for (int j = 0; j < D / 32; ++j)
+#pragma unroll
+        for (int h = 0; h < kDecSub; ++h) {
+          uint32_t a[4], bb[4];
+          e2m1x8_to_f16x2(x[h].k[0][j], a);
+          e2m1x8_to_f16x2(x[h].k[1][j], bb);
+          const bool hi = D == 128 && j >= 2;
+          const uint32_t s0 = scale_f16x2(hi ? x[h].ks[0] >> 8 : x[h].ks[0] & 0xFFu);
+          const uint32_t s1 = scale_f16x2(hi ? x[h].ks[1] >> 8 : x[h].ks[1] & 0xFFu);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            a[i] = hmul2_rn(a[i], s0);
+            bb[i] = hmul2_rn(bb[i], s1);
+          }
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            mma_f16(sc[h][n], a[0], bb[0], a[1], bb[1], qf[n][4 * j], qf[n][4 * j + 1]);
+            mma_f16(sc[h][n], a[2], bb[2], a[3], bb[3], qf[n][4 * j + 2], qf[n][4 * j + 3]);
+          }
+        }
       // exponents of the weights; -inf where a row does not see the key
-      float y[NT][4], top = -CUDART_INF_F;
+      float y[kDecSub][NT][4], top = -CUDART_INF_F;
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) y[n][i] = __fmaf_rn(sc[n][i], c2[n][i & 1], up[n][i & 1]);
-      if (gone || j0 + 15 > s.pos0 || j0 + 16 > s.hi || (p.window > 0 && j0 <= pos_last - p.window)) {
+      for (int h = 0; h < kDecSub; ++h)
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int j = j0 + dec_key(g) + 8 * (i >> 1);
-            const int pos = s.pos0 + static_cast<int>(fast_div(first_row + 8 * n + 2 * t + (i & 1), p.group_div));
-            const bool see = !gone && j <= pos && j < s.hi && (p.window <= 0 || j > pos - p.window);
-            if (!see) y[n][i] = -CUDART_INF_F;
-          }
+          for (int i = 0; i < 4; ++i) y[h][n][i] = __fmaf_rn(sc[h][n][i], c2[n][i & 1], up[n][i & 1]);
+      constexpr int kKeys = 16 * kDecSub;
+      if (gone || j0 + kKeys - 1 > s.pos0 || j0 + kKeys > s.hi || (p.window > 0 && j0 <= pos_last - p.window)) {
+#pragma unroll
+        for (int h = 0; h < kDecSub; ++h)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int j = j0 + 16 * h + dec_key(g) + 8 * (i >> 1);
+              const int pos = s.pos0 + static_cast<int>(fast_div(first_row + 8 * n + 2 * t + (i & 1), p.group_div));
+              const bool see = !((gone >> h) & 1u) && j <= pos && j < s.hi && (p.window <= 0 || j > pos - p.window);
+              if (!see) y[h][n][i] = -CUDART_INF_F;
+            }
       }
       // the sums are rescaled only when a score is kLag above its row's
       // maximum so far
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int h = 0; h < kDecSub; ++h)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) top = fmaxf(top, y[n][i]);
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) top = fmaxf(top, y[h][n][i]);
       if (__any_sync(0xffffffffu, top > kShift + kLag)) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const float x0 = y[n][i] == -CUDART_INF_F ? -CUDART_INF_F : sc[n][i] * c2[n][i];
-            const float x1 = y[n][i + 2] == -CUDART_INF_F ? -CUDART_INF_F : sc[n][i + 2] * c2[n][i];
-            float z = fmaxf(x0, x1);
+            float z = -CUDART_INF_F;
+#pragma unroll
+            for (int h = 0; h < kDecSub; ++h)
+#pragma unroll
+              for (int k = i; k < 4; k += 2)
+                if (y[h][n][k] > -CUDART_INF_F) z = fmaxf(z, sc[h][n][k] * c2[n][i]);
             z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, 4));
             z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, 8));
             z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, 16));
@@ -430,68 +450,77 @@ __global__ void __launch_bounds__(kDecThreads, dec_ctas_per_sm(NT)) attention_de
               o[n][d][i] *= a;
               o[n][d][i + 2] *= a;
             }
-            y[n][i] = x0 + un;
-            y[n][i + 2] = x1 + un;
+#pragma unroll
+            for (int h = 0; h < kDecSub; ++h)
+#pragma unroll
+              for (int k = i; k < 4; k += 2)
+                if (y[h][n][k] > -CUDART_INF_F) y[h][n][k] = __fmaf_rn(sc[h][n][k], c2[n][i], un);
           }
       }
-      uint32_t pb[NT][2];
+      uint32_t pb[kDecSub][NT][2];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const float e0 = ex2(y[n][0]), e1 = ex2(y[n][1]), e2 = ex2(y[n][2]), e3 = ex2(y[n][3]);
-        l[n][0] += e0 + e2;
-        l[n][1] += e1 + e3;
-        pb[n][0] = move_trans(pack_f16x2(e0, e1));
-        pb[n][1] = move_trans(pack_f16x2(e2, e3));
+      for (int h = 0; h < kDecSub; ++h) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const float e0 = ex2(y[h][n][0]), e1 = ex2(y[h][n][1]), e2 = ex2(y[h][n][2]), e3 = ex2(y[h][n][3]);
+          l[n][0] += e0 + e2;
+          l[n][1] += e1 + e3;
+          pb[h][n][0] = move_trans(pack_f16x2(e0, e1));
+          pb[h][n][1] = move_trans(pack_f16x2(e2, e3));
+        }
       }
       // O^T += V^T P^T
-      x.read_values(st, g, t);
-      const uint32_t sa = scale_pair_f16x2(x.vs[0], x.vs[1]), sb = scale_pair_f16x2(x.vs[2], x.vs[3]);
 #pragma unroll
-      for (int j = 0; j < D / 64; ++j) {
-        // bytes {value 2t, value 2t + 1} of elements 0, 2, 4, 6 and 1, 3, 5, 7 of the word
-        constexpr uint32_t kLow = 0x0F0F0F0Fu;
-        uint32_t a0[4], a1[4], b0[4], b1[4];
-        e2m1x8_to_f16x2((x.v[0][j] & kLow) | ((x.v[1][j] << 4) & ~kLow), a0);
-        e2m1x8_to_f16x2(((x.v[0][j] >> 4) & kLow) | (x.v[1][j] & ~kLow), a1);
-        e2m1x8_to_f16x2((x.v[2][j] & kLow) | ((x.v[3][j] << 4) & ~kLow), b0);
-        e2m1x8_to_f16x2(((x.v[2][j] >> 4) & kLow) | (x.v[3][j] & ~kLow), b1);
+      for (int h = 0; h < kDecSub; ++h) {
+        x[h].read_values(st + h * kGroup, g, t);
+        const uint32_t sa = scale_pair_f16x2(x[h].vs[0], x[h].vs[1]), sb = scale_pair_f16x2(x[h].vs[2], x[h].vs[3]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          a0[i] = hmul2_rn(a0[i], sa);
-          a1[i] = hmul2_rn(a1[i], sa);
-          b0[i] = hmul2_rn(b0[i], sb);
-          b1[i] = hmul2_rn(b1[i], sb);
+        for (int j = 0; j < D / 64; ++j) {
+          // bytes {value 2t, value 2t + 1} of elements 0, 2, 4, 6 and 1, 3, 5, 7 of the word
+          constexpr uint32_t kLow = 0x0F0F0F0Fu;
+          uint32_t a0[4], a1[4], b0[4], b1[4];
+          e2m1x8_to_f16x2((x[h].v[0][j] & kLow) | ((x[h].v[1][j] << 4) & ~kLow), a0);
+          e2m1x8_to_f16x2(((x[h].v[0][j] >> 4) & kLow) | (x[h].v[1][j] & ~kLow), a1);
+          e2m1x8_to_f16x2((x[h].v[2][j] & kLow) | ((x[h].v[3][j] << 4) & ~kLow), b0);
+          e2m1x8_to_f16x2(((x[h].v[2][j] >> 4) & kLow) | (x[h].v[3][j] & ~kLow), b1);
 #pragma unroll
-          for (int n = 0; n < NT; ++n) mma_f16(o[n][4 * j + i], a0[i], a1[i], b0[i], b1[i], pb[n][0], pb[n][1]);
+          for (int i = 0; i < 4; ++i) {
+            a0[i] = hmul2_rn(a0[i], sa);
+            a1[i] = hmul2_rn(a1[i], sa);
+            b0[i] = hmul2_rn(b0[i], sb);
+            b1[i] = hmul2_rn(b1[i], sb);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma_f16(o[n][4 * j + i], a0[i], a1[i], b0[i], b1[i], pb[h][n][0], pb[h][n][1]);
+          }
         }
       }
     };
 
     uint32_t gone_cur = gone_now;
+    constexpr int kTurn = 32 / kDecSub;                 // steps of a look-up
     for (int step0 = 0; step0 < steps; step0 += kDecStages) {
 #pragma unroll
       for (int u = 0; u < kDecStages; ++u) {             // step0 + u lies in place u of the ring
         const int step = step0 + u;
         if (step >= steps) break;
-        cp_async_wait<kDecStages - 2>();
-        __syncwarp();                                   // the step has landed, and its predecessor's place is free
-        const int ahead = step + kDecStages - 1;
-        if (u == 1) {                                   // ahead is a multiple of kDecStages
-          if ((ahead & 31) == 16) {
-            rows_next = lookup(ahead + 16 + lane);
+        cp_async_wait<0>();
+        __syncwarp();                                   // the step has landed, and the other place is free
+        const int ahead = step + 1;
+        if (u == 1) {                                   // ahead is even
+          if (ahead % kTurn == kTurn / 2) {
+            rows_next = lookup(kDecSub * (ahead + kTurn / 2) + lane);
             gone_next = __ballot_sync(0xffffffffu, rows_next == kNoRow);
             if (rows_next == kNoRow) rows_next = 0u;
           }
-          if ((ahead & 31) == 0) {
+          if (ahead % kTurn == 0) {
             rows_now = rows_next;
             gone_now = gone_next;
           }
         }
-        const uint32_t row = __shfl_sync(0xffffffffu, rows_now, ahead & 31);
-        if (ahead < steps) copy.load(row, ring_a + (u + kDecStages - 1) % kDecStages * kStage, lane);
+        if (ahead < steps) fetch(ahead, 1 - u);
         cp_async_commit();
-        if (u == 0 && (step & 31) == 0) gone_cur = gone_now;      // ahead has passed into this step's 32
-        attend(ring + u * kStage, j_first + step * kDecTile, (gone_cur >> (step & 31)) & 1u);
+        if (u == 0 && step % kTurn == 0) gone_cur = gone_now;     // ahead has passed into this step's look-up
+        attend(ring + u * kStage, j_first + step * kDecTile, (gone_cur >> (kDecSub * (step % kTurn))) & ((1u << kDecSub) - 1u));
       }
     }
     cp_async_wait<0>();
