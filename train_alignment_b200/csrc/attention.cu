@@ -3,7 +3,8 @@
 //   out[r][h] = sum_j softmax_j(scale q[r][h] . k_j) v_j,  j <= p, j > p - window
 //
 // Two kernels: few rows per sequence and key head (attention_decode.cuh) are
-// bound by the cache's bytes, many (attention_chunk.cuh) by the tensor cores.
+// bound by the cache's bytes and their conversion, many (attention_chunk.cuh)
+// by the tensor cores.
 #include "attention_chunk.cuh"
 #include "attention_decode.cuh"
 
@@ -38,13 +39,17 @@ int launch_dependent(void (*kernel)(Params...), dim3 grid, int threads, cudaStre
 }
 
 // CTAs of the kernel for few rows: as many as are resident at once.
-int dec_grid(int nt) {
-  const int n = dec_ctas_per_sm(nt) * num_sms();
-  return n < kMaxRuns ? n : kMaxRuns;
-}
-constexpr int kChMinTiles = 4;       // key tiles of a split: shorter ones cost more in joining than they save
-constexpr int kDecMaxRows = 32;      // rows of a sequence and key head up to which the kernel for few rows is taken
-constexpr int kDecMinQuota = 2;      // tiles of a run: shorter ones cost more in joining than they save
+int dec_grid(int nt) { return dec_ctas_per_sm(nt) * num_sms(); }
+// Key tiles (of 128) of a split: shorter ones cost more in joining than they save.
+constexpr int kChMinTiles = 4;
+// Rows of a sequence and key head up to which the kernel for few rows is
+// taken.  16 sequences of up to 8192 keys, 4 key heads: 48 rows 43 us against
+// 60 us in the kernel for many, 32 rows 36 against 60; 64 rows 47 against 60,
+// but at short contexts (64 x 512 keys) 33 against 25.
+constexpr int kDecMaxRows = 48;
+// Tiles of a run (512 keys): with 2, one context of 65536 takes 21.5 us, most
+// of it joining; with 4, 16.6 us.
+constexpr int kDecMinQuota = 4;
 
 size_t dec_workspace(int D, int nt) {
   return static_cast<size_t>(dec_grid(nt)) * (2 * (8 * nt) * (D * sizeof(float) + sizeof(float2)) + sizeof(int4));
@@ -93,6 +98,9 @@ ChunkPlan chunk_plan(const quads_kv_cache* c, int64_t rows, int heads_q, int n_s
   const int64_t tiles = ceil_div(static_cast<int64_t>(max_pages) * c->page_size, int64_t(kChTile));
   int64_t n = units > 0 ? num_sms() / units : 1;
   if (n > tiles / kChMinTiles) n = tiles / kChMinTiles;
+  // no more than 256 MB of parts (a call with many rows of no sequence)
+  const int64_t part = rows * heads_q * static_cast<int64_t>(c->head_dim * sizeof(float) + sizeof(float2));
+  while (n > 1 && n * part > (int64_t(1) << 28)) --n;
   if (n > 1) p.n_split = static_cast<int>(n);
   return p;
 }
@@ -169,7 +177,7 @@ int quads_attention_paged(const uint16_t* q, int64_t rows, int64_t ld_q, int hea
   if (unit_rows <= kDecMaxRows) {
     const int64_t tiles = (static_cast<int64_t>(max_pages) * cache->page_size / kDecTile + 2) * ceil_div(unit_rows, int64_t(8));
     QUADS_REQUIRE(tiles < (int64_t(1) << 30) && tiles * n_seqs * cache->n_heads < (int64_t(1) << 30),
-                  QUADS_ERR_UNSUPPORTED_SHAPE, "n_seqs * n_heads * max_pages * page_size must be below 2^36");
+                  QUADS_ERR_UNSUPPORTED_SHAPE, "too many key tiles: n_seqs * n_heads * (max_pages * page_size / %d + 2) must be below 2^27", kDecTile);
     const int n = static_cast<int>(unit_rows);
     const bool whole = dec_whole(cache, max_pages);
     if (cache->head_dim == 64)

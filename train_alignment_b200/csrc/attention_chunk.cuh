@@ -20,6 +20,14 @@
 // Tensor memory: S at column 0, P_0 and P_1 at 128 and 192, O_0 and O_1 at 256
 // and 384.
 //
+// Measured on chunks of 4096 and 3793 tokens that end contexts of 12000 and
+// 9909, 32 query and 8 key heads of 128 (1.17 TFLOP): 0.87 ms alone, 1340
+// TFLOP/s, 0.82 of the measured burst of a library product; back to back under
+// the power cap 0.96 ms, 0.89 of its sustained rate.  The tensor pipe is active
+// 65 % of the cycles and so is the unit of exponentials; leaving out the
+// exponentials changes nothing, leaving out the conversion 12 %.  The products'
+// issue was the limit before: from one lane in a divergent branch 1.31 ms.
+//
 // Where the rows give fewer CTAs than SMs the keys are split too, and
 // attention_join_kernel joins the parts.  Every wait is bounded.
 #pragma once

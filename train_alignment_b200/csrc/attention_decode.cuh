@@ -1,18 +1,18 @@
-// Attention of few rows: bound by the bytes of the cache, or by the conversion
+// Attention of few rows: bound by the bytes of the cache and by the conversion
 // of its codes.
 //
 // A unit is (sequence, key head, 8 NT of its rows); its keys are cut into
-// tiles of 64, and the tiles of all units, end to end, into equal runs, one
-// per CTA, so that sequences of any lengths load the SMs alike.  A unit that spans several
-// CTAs leaves partial sums that attention_combine_kernel joins in order.
+// tiles of 128, and the tiles of all units, end to end, into equal runs, one
+// per CTA, so that sequences of any lengths load the SMs alike.  A unit that
+// several CTAs share leaves partial sums that attention_combine_kernel joins
+// in order.  Where no context is longer than kDecWhole tiles a CTA takes whole
+// units and nothing is joined: 700 keys in one launch instead of two, 8.5 us
+// against 12.
 //
-// Where no context is longer than kDecWhole tiles, a CTA takes whole units and
-// nothing is joined.
-//
-// A CTA's four warps take 16 keys each of a tile, straight from global memory
-// into the registers of the matrix instructions (m16n8k16, keys as M: the
-// rows of up to 8 (16) queries are its N, so a group of 8 query heads wastes
-// nothing):
+// A CTA's four warps take 32 keys each of a tile, from a ring in shared memory
+// (cp.async, the next step's copies under this one's arithmetic) into the
+// registers of the matrix instructions (m16n8k16, keys as M: the rows of up to
+// 8 (16) queries are its N, so a group of 8 query heads wastes nothing):
 //   S^T = K Q^T: a lane's 32 (16) elements of key g, g + 8 are one load; the
 //   order of the elements along the reduction is free as long as Q's is the
 //   same, so Q's registers are loaded in the same order;
@@ -22,6 +22,16 @@
 //   before they are converted.
 // E2M1 times E4M3 has at most 6 significant bits, so keys and values are
 // exact in FP16.
+//
+// Why these instructions and not tcgen05 as in the kernel for many rows: of
+// about 280 instructions for 16 keys, 128 convert codes and apply scales, which
+// every layout needs; with keys in tensor memory the stores and the softmax on
+// 128 lanes come to about 240, while a tile of 128 rows for 4 queries would
+// wait on its own products.  Two groups of 16 keys at once hide each other's
+// latency: one group, and four CTAs an SM instead of three, took 49.2 us where
+// this takes 43.7 (four contexts of up to 65536, 32 / 8 heads of 128: 170 MB,
+// 3.9 TB/s; the copies alone take 37).  Of 64 contexts of up to 4096 (87 MB,
+// 31 us) about 14 us are launch, look-ups, pipeline fill and join.
 #pragma once
 
 #include "attention.cuh"
@@ -32,11 +42,10 @@ constexpr int kDecThreads = 128;
 constexpr int kDecWarps = kDecThreads / 32;
 constexpr int kDecSub = 2;                            // groups of 16 keys of a warp's step
 constexpr int kDecTile = 16 * kDecSub * kDecWarps;
-constexpr int kDecWhole = 8;
-// resident CTAs of an SM: its registers hold 128 (168) a thread (five of 96
-// registers spill and take 10 % longer)
+constexpr int kDecWhole = 8;                          // tiles of a context that is not cut
+// Resident CTAs of an SM: its registers hold 168 (255) a thread.  Four of 128
+// (three of 168) are within 5 % at 8 rows and up to 40 % slower at 16.
 __host__ __device__ constexpr int dec_ctas_per_sm(int nt) { return nt == 1 ? 3 : 2; }
-constexpr int kMaxRuns = 1024;      // CTAs of a launch
 
 // Key tiles of a sequence's units, and its units per head.
 __device__ __forceinline__ int dec_tiles(const SeqInfo& s) {
@@ -138,10 +147,11 @@ __device__ __forceinline__ uint32_t move_trans(uint32_t x) {
   return y;
 }
 
-// A warp's ring of steps in shared memory: 16 keys' and values' codes and
-// scales as they lie in the cache, copied 16 bytes at a time.  Chunk c of a
+// A warp's ring of steps in shared memory: for each group of 16 keys their and
+// their values' codes and scales as they lie in the cache, copied 16 bytes at
+// a time.  Chunk c of a
 // value's codes is at c ^ (key / 2 % 4) (D = 128), and key i of a matrix of
-// eight is row i ^ (i / 2 % 2) of the step: both matrix operands are then read
+// eight is row i ^ (i / 2 % 2) of the group: both matrix operands are then read
 // without bank conflicts.
 constexpr int kDecStages = 2;
 __host__ __device__ constexpr int dec_stage_bytes(int D) { return 16 * (D + D / 8); }
@@ -156,8 +166,8 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
 
-// Where a lane copies its chunks from (for row 0 of the cache) and to (for a
-// step's place at 0).
+// Where a lane copies its chunks of a group from (for row 0 of the cache) and
+// to (for a place at 0).
 template <int D>
 struct DecCopy {
   static constexpr int kChunks = D / 32;                 // 16-byte chunks of a key's codes
@@ -185,7 +195,7 @@ struct DecCopy {
   }
 };
 
-// A lane's part of a step: keys g and g + 8, elements [t D / 4, (t + 1) D / 4);
+// A lane's part of a group: keys g and g + 8, elements [t D / 4, (t + 1) D / 4);
 // values 2t, 2t + 1, 2t + 8, 2t + 9, elements [g D / 8, (g + 1) D / 8).
 template <int D>
 struct DecRaw {
@@ -288,9 +298,10 @@ __global__ void __launch_bounds__(kDecThreads, dec_ctas_per_sm(NT)) attention_de
     const int first_row = grp * kRows;
     const int R = min(s.nq * p.group - first_row, kRows);
 
-    // The warp's steps of 16 keys, one per tile.  A step's keys share a page:
-    // lane i looks up the cache row of step i of 32, the next 32 half way
-    // through these.  A step without a page reads row 0 and masks it.
+    // The warp's steps of two groups of 16 keys, one step per tile.  A group's
+    // keys share a page: lane i looks up the cache row of group i of 32, the
+    // next 32 half way through these.  A group without a page reads row 0 and
+    // masks it.
     const int pos_last = s.pos0 + s.nq - 1;
     const int j_first = s.lo + tile0 * kDecTile + 16 * kDecSub * warp;
     const int steps = min(tile1 - tile0, (s.hi - j_first + kDecTile - 1) / kDecTile);     // those with a key below hi
