@@ -125,6 +125,22 @@ def test_write_and_read(cuda_lib, heads, dim, page, new, kv):
                 np.testing.assert_array_equal(g.double().cpu().numpy(), r)
 
 
+@pytest.mark.parametrize("lead", [0, 8, 16])
+def test_write_from_wider_rows(cuda_lib, lead):
+    """k and v as slices of a projection's rows, at 16- and 32-byte offsets."""
+    heads, dim, rows = 4, 64, 70
+    wide = _randn((rows, lead + 2 * heads * dim + 24), 1)
+    k = wide[:, lead:lead + heads * dim].view(rows, heads, dim)
+    v = wide[:, lead + heads * dim:lead + 2 * heads * dim].view(rows, heads, dim)
+    off, kv, table = R.offsets([50, 20]).to(DEV), torch.tensor([50, 33], dtype=torch.int32, device=DEV), \
+        R.make_table([50, 33], 16, 9, 4, 2).to(DEV)
+    caches = [A.KVCache.empty(9, 16, heads, dim, 3.0, 3.0, DEV) for _ in range(2)]
+    B.kv_cache_write(caches[0], k, v, off, kv, table)
+    B.kv_cache_write(caches[1], k.contiguous(), v.contiguous(), off, kv, table)
+    for n in ("k_codes", "k_scales", "v_codes", "v_scales"):
+        assert torch.equal(getattr(caches[0], n), getattr(caches[1], n)) and getattr(caches[0], n).any()
+
+
 def test_write_and_read_leave_the_rest(cuda_lib):
     """Rows behind the last sequence, negative positions, positions without a
     page: nothing else is written; reading gives zeros without a page and
@@ -220,6 +236,69 @@ def test_pages_and_windows(cuda_lib, dim, page, window):
 def test_chunks(cuda_lib, dim, heads, group, new, kv):
     _attend(heads, group, dim, 32, new, kv, seed=30 + group, extra=3, garbage=True)
     _attend(heads, group, dim, 16, new, kv, window=90, seed=31 + group, garbage=True)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("heads,group,new,kv", [
+    (2, 4, [3, 8, 12, 1, 0, 5], [300, 2000, 1100, 1500, 40, 5]), (1, 16, [3, 1, 2], [4000, 1100, 1025]),
+    (1, 1, [48, 17, 33], [48, 900, 2000]), (3, 6, [8, 3], [8, 1300]), (1, 48, [1, 0, 1], [2100, 0, 700])])
+def test_rows_in_groups(cuda_lib, dim, heads, group, new, kv):
+    """17 to 48 rows of a key head: several units, of which a sequence may have fewer."""
+    _attend(heads, group, dim, 16, new, kv, seed=36, extra=1, garbage=True)
+    _attend(heads, group, dim, 48, new, kv, window=130, seed=37, garbage=True)
+
+
+@pytest.mark.parametrize("heads,n", [(1, 200), (4, 200), (8, 129)])
+def test_many_sequences(cuda_lib, heads, n):
+    """More sequences than one scan takes; units by themselves and by the CTA that begins them; sequences without rows."""
+    kv = [1 + (37 * b) % 1500 for b in range(n)]
+    new = [0 if b % 7 == 3 else 1 + b % 3 for b in range(n)]
+    _attend(heads, 4, 64, 16, new, [max(k, m) for k, m in zip(kv, new)], seed=38)
+
+
+@pytest.mark.parametrize("new", [[1, 1], [12, 3], [200, 60]])
+def test_no_pages(cuda_lib, new):
+    """A cache without pages, a table without columns, a table that ends before the sequence does."""
+    for dim in (64, 128):
+        t = R.make_cache(4, 2, 16, dim, 1, DEV)
+        none = {n: (x[:0].contiguous() if x.dim() == 4 else x) for n, x in t.items()}
+        off, lens = R.offsets(new).to(DEV), torch.tensor([300, 70], dtype=torch.int32, device=DEV)
+        rows = sum(new)
+        q = _randn((rows, 8, dim), 2)
+        for cache, table in ((none, torch.zeros((2, 30), dtype=torch.int32)), (t, torch.zeros((2, 0), dtype=torch.int32)),
+                             (none, torch.zeros((2, 0), dtype=torch.int32))):
+            out, lse = torch.full_like(q, 4.0), torch.zeros((rows, 8), device=DEV)
+            B.attention_paged(q, _cache(cache), off, lens, table.to(DEV), max(new), out=out, lse=lse)
+            assert not out.any() and torch.isneginf(lse).all()
+            k, v = B.kv_cache_read(_cache(cache), off, table.to(DEV), rows)
+            assert not k.any() and not v.any()
+            B.kv_cache_write(_cache(cache), q[:, :2], q[:, 2:4], off, lens, table.to(DEV))
+        # 2 pages of the sequences' 19 and 5
+        table = torch.tensor([[2, 0], [1, 3]], dtype=torch.int32)
+        ref = R.attention64(q, t, off, lens, table, 0.1)
+        lse = torch.empty((rows, 8), device=DEV)
+        out = B.attention_paged(q, _cache(t), off, lens, table.to(DEV), max(new), scale=0.1, lse=lse)
+        tol, tol_lse = R.attention_bounds(*ref, dim)
+        assert ((out.double() - ref[0]).abs() <= tol).all() and ((lse.double() - ref[1]).abs() <= tol_lse).all()
+    assert B.device_status() == B.OK
+
+
+def test_a_longer_sequence_than_max_q_len(cuda_lib):
+    """Its rows past max_q_len are left as they are; the others are right."""
+    for cap, new in ((2, [5, 1]), (20, [150, 20])):
+        t = R.make_cache(40, 2, 16, 128, 3, DEV)
+        kv = [300, 64]
+        off, lens = R.offsets(new).to(DEV), torch.tensor(kv, dtype=torch.int32, device=DEV)
+        table = R.make_table(kv, 16, 40, 19, 4)
+        q = _randn((sum(new), 8, 128), 5)
+        ref = R.attention64(q, t, off, lens, table, 0.1)
+        out = torch.full_like(q, 6.0)
+        B.attention_paged(q, _cache(t), off, lens, table.to(DEV), cap, scale=0.1, out=out)
+        tol, _ = R.attention_bounds(*ref, 128)
+        done = torch.zeros(sum(new), dtype=torch.bool, device=DEV)
+        done[:cap] = True
+        done[new[0]:] = True
+        assert ((out.double() - ref[0]).abs() <= tol)[done].all() and (out[~done] == 6.0).all()
 
 
 @pytest.mark.parametrize("new", [[1, 1, 1, 1], [4, 2, 3, 4], [40, 41, 42, 43]])

@@ -27,7 +27,7 @@ def desc(**kw):
 
 
 BAD_CACHES = [dict(n_pages=-1), dict(n_pages=1 << 31), dict(page_size=0), dict(page_size=24), dict(page_size=1 << 17),
-              dict(n_heads=0), dict(n_heads=2000), dict(head_dim=96), dict(head_dim=0), dict(k_codes=None), dict(v_scales=None),
+              dict(n_heads=0), dict(n_heads=2000), dict(head_dim=96), dict(head_dim=0), dict(n_pages=1 << 30, page_size=64), dict(k_codes=None), dict(v_scales=None),
               dict(g_k=None), dict(v_codes=P + 8)]
 
 
@@ -52,11 +52,13 @@ def rope(l, q=P, ld_q=256, hq=2, k=P, ld_k=128, hk=1, T=4, dim=128, pos=P, freq=
 BAD = [(write, dict(rows=-1)), (write, dict(ld_k=250)), (write, dict(ld_v=128)), (write, dict(k=None)), (write, dict(kv=None)),
        (write, dict(v=P + 2)), (write, dict(n=-1)), (write, dict(n=70000)), (write, dict(off=None)), (write, dict(table=None)),
        (write, dict(pages=-1)),
-       (read, dict(rows=-1)), (read, dict(dt=2)), (read, dict(k=None, v=None)), (read, dict(k=P + 4)), (read, dict(off=None)),
+       (read, dict(rows=-1)), (read, dict(dt=2)), (read, dict(k=None, v=None)), (read, dict(k=P + 16)), (read, dict(off=None)),
        (attend, dict(rows=1 << 31)), (attend, dict(hq=7)), (attend, dict(hq=0)), (attend, dict(hq=8192, ld=1 << 21)),
        (attend, dict(ld=1000)), (attend, dict(ld=1028)), (attend, dict(window=-1)), (attend, dict(mq=-1)),
        (attend, dict(scale=float("nan"))), (attend, dict(scale=float("inf"))), (attend, dict(q=None)), (attend, dict(out=None)),
-       (attend, dict(kv=None)), (attend, dict(q=P + 8)), (attend, dict(out=P + 8)),
+       (attend, dict(kv=None)), (attend, dict(pages=1000, ws=None)), (attend, dict(pages=1000, ws_bytes=100)),
+       (attend, dict(pages=1000, ws=P + 4)), (attend, dict(rows=100, mq=50, pages=1000, ws_bytes=100)),
+       (attend, dict(n=60000, pages=2000000)), (attend, dict(q=P + 8)), (attend, dict(out=P + 8)),
        (rope, dict(T=-1)), (rope, dict(hq=0, hk=0)), (rope, dict(dim=120)), (rope, dict(dim=2048)), (rope, dict(rot=8)),
        (rope, dict(rot=144)), (rope, dict(ld_q=128)), (rope, dict(ldo_k=132)), (rope, dict(q=None)), (rope, dict(ok=None)),
        (rope, dict(pos=None)), (rope, dict(freq=None)), (rope, dict(oq=P + 8))]

@@ -153,8 +153,7 @@ int quads_attention_paged(const uint16_t* q, int64_t rows, int64_t ld_q, int hea
   QUADS_TRY(check_cache(cache));
   QUADS_TRY(check_seqs(row_off, block_table, n_seqs, max_pages));
   QUADS_REQUIRE(rows >= 0 && rows < (int64_t(1) << 30), QUADS_ERR_INVALID_ARG, "rows must be in [0, 2^30)");
-  QUADS_REQUIRE(rows * cache->n_heads < (int64_t(1) << 31), QUADS_ERR_UNSUPPORTED_SHAPE,
-                "rows * n_heads must be below 2^31");
+  QUADS_REQUIRE(rows * heads_q < (int64_t(1) << 31), QUADS_ERR_UNSUPPORTED_SHAPE, "rows * heads_q must be below 2^31");
   QUADS_REQUIRE(heads_q >= 1 && heads_q <= 4096 && heads_q % cache->n_heads == 0, QUADS_ERR_UNSUPPORTED_SHAPE,
                 "heads_q (%d) must be a multiple of the cache's %d heads, at most 4096", heads_q, cache->n_heads);
   QUADS_REQUIRE(ld_q >= static_cast<int64_t>(heads_q) * cache->head_dim && ld_q % 8 == 0, QUADS_ERR_INVALID_ARG,

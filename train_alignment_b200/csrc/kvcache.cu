@@ -121,7 +121,8 @@ __device__ __forceinline__ Block block_of(const BlockMap& m, int i) {
 // --------------------------------------------------------------- the write
 // One thread per block of 16 elements: 32 bytes in (one access where the rows
 // are 32-byte aligned), 8 + 1 bytes out.  Bound by HBM: 2 bytes read and
-// 0.5625 written per element.  16400 tokens of 8 heads of 128 (86 MB): 24 us.
+// 0.5625 written per element.  16493 tokens of 8 heads of 128 (87 MB): 21 us,
+// three quarters of the issue slots taken.
 template <bool kWide>
 __global__ void __launch_bounds__(kThreads) kv_write_kernel(CacheArgs c, const uint16_t* __restrict__ k,
                                                             const uint16_t* __restrict__ v, int64_t rows,
@@ -150,11 +151,12 @@ __global__ void __launch_bounds__(kThreads) kv_write_kernel(CacheArgs c, const u
 }
 
 // ---------------------------------------------------------------- the read
-// One thread per block of 16 elements, four blocks in flight: 8 + 1 bytes in,
+// One thread per block of 16 elements, two blocks in flight: 8 + 1 bytes in,
 // 32 (BF16) or 64 (FP32) out in 32-byte stores.  Bound by HBM: 0.5625 bytes
 // read and 2 or 4 written per element.  Eight contexts of up to 8192 tokens, 8
-// heads of 128, to BF16 (262 MB): 54 us, 4.9 TB/s.
-constexpr int kReadUnroll = 4;
+// heads of 128, to BF16 (262 MB): 50 us, 5.2 TB/s (CTAs of twice the rows and
+// four blocks in flight: 54).
+constexpr int kReadUnroll = 2;
 
 template <bool kF32>
 __global__ void __launch_bounds__(kThreads) kv_read_kernel(CacheArgs c, void* __restrict__ k_out,
@@ -367,7 +369,7 @@ int quads_kv_cache_read(const quads_kv_cache* cache, const int32_t* row_off, con
   const CacheArgs c = cache_args(cache, block_table, n_seqs, max_pages);
   const bool f32 = out_dtype == QUADS_OUT_F32;
   const BlockMap map = block_map(cache, (k_out != nullptr) + (v_out != nullptr));
-  const int per = rows_per_cta(rows, static_cast<int>(map.row_div.d), 2048);
+  const int per = rows_per_cta(rows, static_cast<int>(map.row_div.d), 1024);
   const unsigned grid = static_cast<unsigned>(ceil_div(rows, int64_t(per)));
   if (f32)
     kv_read_kernel<true><<<grid, kThreads, 0, stream>>>(c, k_out, v_out, rows, map, row_off, start, per);
