@@ -631,8 +631,8 @@ typedef struct quads_kv_cache {
  * above a head's calibrated range saturate).  k, v: BF16 [rows][n_heads][D],
  * rows ld_k and ld_v elements apart (multiples of 8), 16-byte aligned, finite.
  * Rows without a page or with a negative position are dropped.  Two rows of
- * one call that name the same place of a page leave it undefined (each block
- * may come from either). */
+ * one call that name the same place of a page (a page twice among those
+ * written) leave the values there undefined. */
 int quads_kv_cache_write(const quads_kv_cache* cache, const uint16_t* k, const uint16_t* v, int64_t rows,
                          int64_t ld_k, int64_t ld_v, const int32_t* row_off, const int32_t* kv_len,
                          const int32_t* block_table, int n_seqs, int max_pages, quads_stream_t stream);
@@ -665,7 +665,7 @@ int quads_rope(const uint16_t* q, int64_t ld_q, int heads_q, const uint16_t* k, 
  * position) and, when window > 0, j > p - window; k and v are the cached
  * values of head h / (heads_q / n_heads).  A row with no such j gets zeros.
  *   q, out    BF16 [rows][heads_q][D], q's rows ld_q elements apart
- *             (a multiple of 8), out's contiguous; 16-byte aligned.  heads_q
+ *             (a multiple of 8) and finite, out's contiguous; 16-byte aligned.  heads_q
  *             is a multiple of n_heads.  out must not overlap q.
  *   max_q_len at least the rows of the longest sequence (a longer sequence's
  *             rows past it are not computed); the work is laid out by it.

@@ -110,10 +110,22 @@ size_t chunk_workspace(const quads_kv_cache* c, int64_t rows, int heads_q, int n
   return static_cast<size_t>(n_split) * rows * heads_q * (c->head_dim * sizeof(float) + sizeof(float2));
 }
 
+// The softmax warpgroups wait for registers that the others give up, which adds
+// up only if the kernel was compiled to 128 a thread.
+template <int D>
+bool chunk_registers_add_up() {
+  static const bool ok = [] {
+    cudaFuncAttributes a{};
+    return cudaFuncGetAttributes(&a, attention_chunk_kernel<D>) == cudaSuccess && a.numRegs == kChRegs;
+  }();
+  return ok;
+}
+
 template <int D>
 int launch_chunk(AttnArgs p, const ChunkPlan& plan, void* ws, cudaStream_t stream) {
   p.part_o = static_cast<float*>(ws);
   p.part_ml = reinterpret_cast<float2*>(p.part_o + static_cast<size_t>(plan.n_split) * p.rows * p.hq * D);
+  QUADS_REQUIRE(chunk_registers_add_up<D>(), QUADS_ERR_CUDA, "attention_chunk_kernel is not compiled to %d registers", kChRegs);
   const int smem = ch_smem_bytes(D);
   if (cudaFuncSetAttribute(attention_chunk_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return check_launch("attention_chunk_kernel attributes");

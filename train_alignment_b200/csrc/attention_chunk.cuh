@@ -43,8 +43,8 @@ constexpr int kChSoftWarps = 8;
 constexpr int kChConvWarp = 8, kChConvWarps = 4;
 constexpr int kChMmaWarp = 12;
 constexpr int kChThreads = 512;                  // four warpgroups of 128 registers a thread, which they share out:
-constexpr int kChSoftRegs = 192, kChConvRegs = 88, kChMmaRegs = 40;
-static_assert(2 * kChSoftRegs + kChConvRegs + kChMmaRegs <= 4 * 128, "registers of the four warpgroups");
+constexpr int kChRegs = 128, kChSoftRegs = 192, kChConvRegs = 88, kChMmaRegs = 40;
+static_assert(2 * kChSoftRegs + kChConvRegs + kChMmaRegs <= 4 * kChRegs, "registers of the four warpgroups");
 constexpr int kChStages = 2;
 constexpr uint32_t kChPCol = 128, kChOCol = 256;   // P_i at kChPCol + 64 i, O_i at kChOCol + 128 i
 constexpr uint64_t kChTimeoutNs = 4000000000ull, kChDrainNs = 500000000ull;
