@@ -238,6 +238,7 @@ struct RopeArgs {
   const double* freq;
   int hq, hk, D, rot;
   float mscale, sign;
+  FastDiv half_div, row_div, head_div;     // by rot / 2, and by the items of a row and of a head
 };
 
 __device__ __forceinline__ void rotate2(uint32_t a, uint32_t b, const float2 (&cs)[2], uint32_t& ra, uint32_t& rb) {
@@ -247,19 +248,38 @@ __device__ __forceinline__ void rotate2(uint32_t a, uint32_t b, const float2 (&c
   rb = pack_bf16x2(b0 * cs[0].x + a0 * cs[0].y, b1 * cs[1].x + a1 * cs[1].y);
 }
 
+// kVec elements of each side of kVec pairs: 16- or 32-byte accesses.
+template <int kVec>
+__device__ __forceinline__ void rope_load(const uint16_t* p, uint32_t (&w)[kVec / 2]) {
+  if constexpr (kVec == 16) {
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                 : "l"(p)
+                 : "memory");
+  } else {
+    const uint4 a = *reinterpret_cast<const uint4*>(p);              // plain loads: out may be in
+    w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+  }
+}
+template <int kVec>
+__device__ __forceinline__ void rope_store(uint16_t* p, const uint32_t (&w)[kVec / 2]) {
+  if constexpr (kVec == 16) store_32b(p, w);
+  else *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // A CTA turns `per_cta` tokens: it fills a table of {m cos, m sin} for its
 // tokens (the angle pos * freq in turns, in 64 bits, reduced to [-1/2, 1/2]
-// before it is rounded to 32), then each thread takes 16 elements of a head:
-// 8 pairs.  Bound by HBM: 4 bytes per element, in and out.  16384 tokens of 40
-// heads of 128 (336 MB): 63 us, 5.3 TB/s.
-template <bool kInterleaved>
+// before it is rounded to 32), then each thread takes 2 kVec elements of a
+// head: kVec pairs.  Bound by HBM: 4 bytes per element, in and out.  16384
+// tokens of 40 heads of 128 (336 MB): 61 us, 5.5 TB/s (16-byte accesses: 63).
+template <bool kInterleaved, int kVec>
 __global__ void __launch_bounds__(kThreads) rope_kernel(RopeArgs p, int per_cta) {
   extern __shared__ float2 cs_s[];                     // [per_cta][rot / 2]
   const int half = p.rot / 2;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * per_cta;
   const int n = static_cast<int>(min(static_cast<int64_t>(per_cta), p.T - t0));
   for (int i = threadIdx.x; i < n * half; i += kThreads) {
-    const int t = i / half, f = i - t * half;
+    const int t = static_cast<int>(fast_div(i, p.half_div)), f = i - t * half;
     double turns = static_cast<double>(__ldg(reinterpret_cast<const long long*>(p.pos) + t0 + t)) *
                    (__ldg(p.freq + f) * 0.15915494309189533577);
     turns -= rint(turns);
@@ -268,42 +288,42 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(RopeArgs p, int per_cta)
     cs_s[i] = make_float2(p.mscale * c, p.sign * (p.mscale * s));
   }
   __syncthreads();
-  const int nv = p.D / 16, per_row = (p.hq + p.hk) * nv;
+  const int per_row = static_cast<int>(p.row_div.d), nv = static_cast<int>(p.head_div.d);
   for (int i = threadIdx.x; i < n * per_row; i += kThreads) {
-    const int t = i / per_row, j = i - t * per_row;
-    int head = j / nv;
+    const int t = static_cast<int>(fast_div(i, p.row_div)), j = i - t * per_row;
+    int head = static_cast<int>(fast_div(j, p.head_div));
     const int x = j - head * nv;
     const bool is_k = head >= p.hq;
     if (is_k) head -= p.hq;
     const uint16_t* src = (is_k ? p.k + (t0 + t) * p.ld_k : p.q + (t0 + t) * p.ld_q) + head * p.D;
     uint16_t* dst = (is_k ? p.k_out + (t0 + t) * p.ld_ko : p.q_out + (t0 + t) * p.ld_qo) + head * p.D;
-    // the thread's two groups of 8 elements: both of its pairs' sides in the
-    // half layout, 16 neighbours in the interleaved one and past rot
-    const bool turned = x < p.rot / 16;
-    const int e0 = (!kInterleaved && turned) ? 8 * x : 16 * x;
-    const int e1 = (!kInterleaved && turned) ? half + 8 * x : 16 * x + 8;
-    const uint4 a = *reinterpret_cast<const uint4*>(src + e0);       // plain loads: out may be in
-    const uint4 b = *reinterpret_cast<const uint4*>(src + e1);
-    uint32_t u[4] = {a.x, a.y, a.z, a.w}, w[4] = {b.x, b.y, b.z, b.w};
+    // the thread's two groups of kVec elements: both of its pairs' sides in the
+    // half layout, 2 kVec neighbours in the interleaved one and past rot
+    const bool turned = x < p.rot / (2 * kVec);
+    const int e0 = (!kInterleaved && turned) ? kVec * x : 2 * kVec * x;
+    const int e1 = (!kInterleaved && turned) ? half + kVec * x : 2 * kVec * x + kVec;
+    uint32_t u[kVec / 2], w[kVec / 2];
+    rope_load<kVec>(src + e0, u);
+    rope_load<kVec>(src + e1, w);
     if (turned) {
-      const float2* cs = cs_s + t * half + 8 * x;
+      const float2* cs = cs_s + t * half + kVec * x;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
+      for (int e = 0; e < kVec / 2; ++e) {
+        const float2 c2[2] = {cs[2 * e], cs[2 * e + 1]};
         if constexpr (kInterleaved) {                  // one pair per word
-          uint32_t* const g = e < 2 ? u + 2 * e : w + 2 * (e - 2);
-          const float2 c2[2] = {cs[2 * e], cs[2 * e + 1]};
+          uint32_t& a = e < kVec / 4 ? u[2 * e] : w[2 * e - kVec / 2];
+          uint32_t& b = e < kVec / 4 ? u[2 * e + 1] : w[2 * e + 1 - kVec / 2];
           uint32_t ra, rb;
-          rotate2(__byte_perm(g[0], g[1], 0x5410), __byte_perm(g[0], g[1], 0x7632), c2, ra, rb);
-          g[0] = __byte_perm(ra, rb, 0x5410);
-          g[1] = __byte_perm(ra, rb, 0x7632);
+          rotate2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632), c2, ra, rb);
+          a = __byte_perm(ra, rb, 0x5410);
+          b = __byte_perm(ra, rb, 0x7632);
         } else {
-          const float2 c2[2] = {cs[2 * e], cs[2 * e + 1]};
           rotate2(u[e], w[e], c2, u[e], w[e]);
         }
       }
     }
-    *reinterpret_cast<uint4*>(dst + e0) = make_uint4(u[0], u[1], u[2], u[3]);
-    *reinterpret_cast<uint4*>(dst + e1) = make_uint4(w[0], w[1], w[2], w[3]);
+    rope_store<kVec>(dst + e0, u);
+    rope_store<kVec>(dst + e1, w);
   }
 }
 
@@ -408,14 +428,24 @@ int quads_rope(const uint16_t* q, int64_t ld_q, int heads_q, const uint16_t* k, 
   p.pos = positions; p.freq = freq;
   p.hq = heads_q; p.hk = heads_k; p.D = head_dim; p.rot = rot_dim;
   p.mscale = mscale; p.sign = inverse ? -1.0f : 1.0f;
-  int per = rows_per_cta(T, (heads_q + heads_k) * head_dim / 16, 1024);
+  auto wide = [](const void* a, int64_t ld) { return aligned(a, 32) && ld % 16 == 0; };
+  const bool vec16 = rot_dim % 32 == 0 && head_dim % 32 == 0 && wide(q, ld_q) && wide(k, ld_k) && wide(q_out, ld_q_out) &&
+                     wide(k_out, ld_k_out);
+  const int nv = head_dim / (vec16 ? 32 : 16), per_row = (heads_q + heads_k) * nv;
+  p.half_div = make_fastdiv(static_cast<uint32_t>(rot_dim / 2));
+  p.row_div = make_fastdiv(static_cast<uint32_t>(per_row));
+  p.head_div = make_fastdiv(static_cast<uint32_t>(nv));
+  int per = rows_per_cta(T, per_row, 1024);
   per = per < 12288 / rot_dim ? per : 12288 / rot_dim;                               // table of at most 48 KB
   const size_t smem = static_cast<size_t>(per) * (rot_dim / 2) * sizeof(float2);
   const unsigned grid = static_cast<unsigned>(ceil_div(T, int64_t(per)));
-  if (interleaved)
-    rope_kernel<true><<<grid, kThreads, smem, stream>>>(p, per);
-  else
-    rope_kernel<false><<<grid, kThreads, smem, stream>>>(p, per);
+  if (vec16) {
+    if (interleaved) rope_kernel<true, 16><<<grid, kThreads, smem, stream>>>(p, per);
+    else rope_kernel<false, 16><<<grid, kThreads, smem, stream>>>(p, per);
+  } else {
+    if (interleaved) rope_kernel<true, 8><<<grid, kThreads, smem, stream>>>(p, per);
+    else rope_kernel<false, 8><<<grid, kThreads, smem, stream>>>(p, per);
+  }
   count_launches(1);
   return check_launch("rope_kernel");
 }
