@@ -646,7 +646,8 @@ int quads_kv_cache_read(const quads_kv_cache* cache, const int32_t* row_off, con
                         void* v_out, int out_dtype, quads_stream_t stream);
 /* Rotary positions of queries and keys (NULL and 0 heads: without that one).
  * BF16 rows of heads_q (heads_k) heads of head_dim elements, ld elements
- * apart (multiples of 8), 16-byte aligned; the outputs may be the inputs.
+ * apart (multiples of 8), 16-byte aligned; q_out may be q and k_out k, without
+ * any other overlap.
  * The first rot_dim elements of a head turn in pairs f = 0 .. rot_dim / 2 - 1
  * of elements (f, f + rot_dim / 2), or (2f, 2f + 1) when interleaved:
  *   a' = m (a cos t - b sin t), b' = m (b cos t + a sin t),
@@ -663,9 +664,10 @@ int quads_rope(const uint16_t* q, int64_t ld_q, int heads_q, const uint16_t* k, 
  *   out[r][h] = bf16(sum_j softmax_j(scale q[r][h] . k_j) v_j)
  * over the positions j of r's sequence that have a page, j <= p (r's own
  * position) and, when window > 0, j > p - window; k and v are the cached
- * values of head h / (heads_q / n_heads).  A row with no such j gets zeros.
+ * values of head h / (heads_q / n_heads).  A row with no such j gets zeros;
+ * otherwise a NaN in q[r][h] or in the head's decode scales gives NaNs.
  *   q, out    BF16 [rows][heads_q][D], q's rows ld_q elements apart
- *             (a multiple of 8) and finite, out's contiguous; 16-byte aligned.  heads_q
+ *             (a multiple of 8), out's contiguous; 16-byte aligned.  heads_q
  *             is a multiple of n_heads.  out must not overlap q.
  *   max_q_len at least the rows of the longest sequence (a longer sequence's
  *             rows past it are not computed); the work is laid out by it.

@@ -1,5 +1,7 @@
 """The paged NVFP4 KV cache, the attention over it and rotary positions on the
 GPU, against the oracle and against 64-bit torch."""
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -307,6 +309,42 @@ def test_rows_that_see_nothing(cuda_lib, new):
     for dim in (64, 128):
         _attend(2, 2, dim, 16, new, [0, 3, 100, 64], seed=40, absent=[(2, j) for j in range(7)], garbage=True)
         _attend(2, 2, dim, 16, new, [17, -5, 100, 200], seed=41, absent=[(2, 0), (2, 3), (3, 12)], window=20, garbage=True)
+
+
+@pytest.mark.parametrize("new,kv", [([1, 1, 1], [300, 90, 1000]), ([2, 1, 2], [5000, 0, 4000]), ([100, 30, 77], [400, 20, 1000]),
+                                    ([900, 5, 1200], [900, 5, 1200])])
+def test_not_a_number(cuda_lib, new, kv):
+    """A NaN in a query or a decode scale shows in its row and head and nowhere else; rows without keys stay zeros."""
+    for dim in (64, 128):
+        t = R.make_cache(700, 2, 16, dim, 70, DEV)
+        off, lens = R.offsets(new).to(DEV), torch.tensor(kv, dtype=torch.int32, device=DEV)
+        table = R.make_table(kv, 16, 700, max(-(-n // 16) for n in kv), 71).to(DEV)
+        rows = sum(new)
+        q = _randn((rows, 8, dim), 72)
+        def run(q, t):
+            lse = torch.full((rows, 8), 5.0, device=DEV)
+            return B.attention_paged(q, _cache(t), off, lens, table, max(new), lse=lse), lse
+        ref = R.attention64(q, t, off, lens, table, dim ** -0.5)
+        tol, tol_lse = R.attention_bounds(*ref, dim)
+        some = ~torch.isneginf(ref[1])
+        bad = torch.zeros((rows, 8), dtype=torch.bool, device=DEV)
+        bad[0, 3] = bad[rows - 1, 0] = bad[new[0], 5] = True
+        qn = q.clone()
+        qn[0, 3, 7] = qn[rows - 1, 0, 0] = qn[new[0], 5, dim - 1] = math.nan
+        for name in (None, "g_k", "g_v"):
+            if name is not None:
+                bad = torch.zeros((rows, 8), dtype=torch.bool, device=DEV)
+                bad[:, 4:] = True
+                g = t[name].clone()
+                g[1] = math.nan
+            out, lse = run(qn, t) if name is None else run(q, {**t, name: g})
+            hit = bad & some
+            assert out[hit].isnan().all() and (name == "g_v" or lse[hit].isnan().all())
+            assert ((out.double() - ref[0]).abs() <= tol)[~hit].all() and not out[~some].any()
+            if name != "g_v":
+                assert ((lse.double() - ref[1]).abs() <= tol_lse)[~hit & some].all()
+            assert torch.equal(torch.isneginf(lse), ~some)
+    assert B.device_status() == B.OK
 
 
 @pytest.mark.parametrize("dim", [64, 128])

@@ -81,18 +81,6 @@ __device__ __forceinline__ bool ch_wait(uint32_t bar, uint32_t parity, volatile 
   }
 }
 
-__device__ __forceinline__ void tmem_store32(uint32_t taddr, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
-}
-
 // ch_wait by a whole warp that goes on together.
 __device__ __forceinline__ bool ch_wait_warp(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
   return __all_sync(0xffffffffu, ch_wait(bar, parity, abort_flag));
@@ -285,9 +273,10 @@ __global__ void __launch_bounds__(kChThreads, 1) attention_chunk_kernel(AttnArgs
         }
         const uint32_t e = row_exponent(max(mx & 0xFFFFu, mx >> 16));
         const float down = exp_field_down(e);
-        // the factor of the row's scores (to powers of two), positive: its sign goes to the queries
+        // the factor of the row's scores (to powers of two), positive: its sign goes to the queries, and so
+        // does a NaN, which would reach masked scores too
         c2 = p.scale * kLog2e * kScaleUnit * __ldg(p.c.g_k + u.head) * exp_field_up(e);
-        const float sign = c2 < 0.0f ? -down : down;
+        const float sign = c2 < 0.0f ? -down : c2 == c2 ? down : c2;
         c2 = fmaxf(fabsf(c2), 1e-37f);                  // not zero, which times -inf were NaN
         const uint32_t dst = q_s + i * kTB + r * 128;
 #pragma unroll
@@ -414,8 +403,8 @@ __global__ void __launch_bounds__(kChThreads, 1) attention_chunk_kernel(AttnArgs
               }
             }
         } else {
-          const float inv = l > 0.0f ? kScaleUnit * __ldg(p.c.g_v + u.head) / l : 0.0f;
-          if (valid && p.lse != nullptr) p.lse[orow] = l > 0.0f ? -up * kLn2 + logf(l) : -CUDART_INF_F;
+          const float inv = l != 0.0f ? kScaleUnit * __ldg(p.c.g_v + u.head) / l : 0.0f;
+          if (valid && p.lse != nullptr) p.lse[orow] = l != 0.0f ? -up * kLn2 + logf(l) : -CUDART_INF_F;
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             uint32_t x[32];
@@ -432,7 +421,7 @@ __global__ void __launch_bounds__(kChThreads, 1) attention_chunk_kernel(AttnArgs
                 for (int e = 0; e < 4; ++e) {
                   const int y = 8 * k + 2 * e;
                   // rows without a key: zeros, whatever the accumulator holds
-                  w[e] = l > 0.0f && some ? pack_bf16x2(__uint_as_float(x[y]) * inv, __uint_as_float(x[y + 1]) * inv) : 0u;
+                  w[e] = l != 0.0f && some ? pack_bf16x2(__uint_as_float(x[y]) * inv, __uint_as_float(x[y + 1]) * inv) : 0u;
                 }
                 dst[k] = make_uint4(w[0], w[1], w[2], w[3]);
               }
@@ -611,7 +600,7 @@ __global__ void __launch_bounds__(256) attention_join_kernel(AttnArgs p, int n_s
     float f = 0.0f;
     if (i0 + lane < n_split) {
       const float2 ml = __ldcg(p.part_ml + at + (i0 + lane) * step);
-      f = ml.y > 0.0f ? ex2(ml.x - m) : 0.0f;           // a part without keys has no sums
+      f = ml.y != 0.0f ? ex2(ml.x - m) : 0.0f;           // a part without keys has no sums
       l += ml.y * f;
     }
     const int n = min(32, n_split - i0);
@@ -627,16 +616,16 @@ __global__ void __launch_bounds__(256) attention_join_kernel(AttnArgs p, int n_s
         y[0] = v.x; y[1] = v.y;
       }
 #pragma unroll
-      for (int e = 0; e < kE; ++e) o[e] = w > 0.0f ? __fmaf_rn(y[e], w, o[e]) : o[e];
+      for (int e = 0; e < kE; ++e) o[e] = w != 0.0f ? __fmaf_rn(y[e], w, o[e]) : o[e];
     }
   }
 #pragma unroll
   for (int k = 16; k; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
-  const float inv = l > 0.0f ? kScaleUnit * __ldg(p.c.g_v + h / p.group) / l : 0.0f;
+  const float inv = l != 0.0f ? kScaleUnit * __ldg(p.c.g_v + h / p.group) / l : 0.0f;
   uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + at * D + lane * kE);
 #pragma unroll
   for (int e = 0; e < kE / 2; ++e) dst[e] = pack_bf16x2(o[2 * e] * inv, o[2 * e + 1] * inv);
-  if (lane == 0 && p.lse != nullptr) p.lse[at] = l > 0.0f ? (m - kShift) * kLn2 + logf(l) : -CUDART_INF_F;
+  if (lane == 0 && p.lse != nullptr) p.lse[at] = l != 0.0f ? (m - kShift) * kLn2 + logf(l) : -CUDART_INF_F;
 }
 
 }  // namespace quads

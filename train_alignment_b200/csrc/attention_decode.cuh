@@ -149,10 +149,9 @@ __device__ __forceinline__ uint32_t move_trans(uint32_t x) {
 
 // A warp's ring of steps in shared memory: for each group of 16 keys their and
 // their values' codes and scales as they lie in the cache, copied 16 bytes at
-// a time.  Chunk c of a
-// value's codes is at c ^ (key / 2 % 4) (D = 128), and key i of a matrix of
-// eight is row i ^ (i / 2 % 2) of the group: both matrix operands are then read
-// without bank conflicts.
+// a time.  Chunk c of a value's codes is at c ^ (key / 2 % 4) (D = 128), and
+// key i of a matrix of eight is row i ^ (i / 2 % 2) of the group: both matrix
+// operands are then read without bank conflicts.
 constexpr int kDecStages = 2;
 __host__ __device__ constexpr int dec_stage_bytes(int D) { return 16 * (D + D / 8); }
 __device__ __forceinline__ int dec_key(int i) { return i ^ ((i >> 1) & 1); }
@@ -245,7 +244,7 @@ __global__ void __launch_bounds__(kDecThreads, dec_ctas_per_sm(NT)) attention_de
   __shared__ __align__(128) uint8_t buf_s[kRing > kJoin ? kRing : kJoin];    // the warps' rings, then their sums
   float (*const o_s)[kRows][D] = reinterpret_cast<float (*)[kRows][D]>(buf_s);
   __shared__ float2 ml_s[kDecWarps][kRows];
-  __shared__ float f_s[kDecWarps][kRows];               // weight of each warp's sums; then 1 / l in [0]
+  __shared__ float f_s[kDecWarps][kRows];               // weight of each warp's sums (of a whole unit: over the row's sum)
   __shared__ DecPlan<kRows> plan;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
@@ -578,13 +577,13 @@ __global__ void __launch_bounds__(kDecThreads, dec_ctas_per_sm(NT)) attention_de
         ll += ml_s[i][r].y * f;
       }
       if (whole) {
-        const float inv = ll > 0.0f ? kScaleUnit * __ldg(p.c.g_v + head) / ll : 0.0f;
+        const float inv = ll != 0.0f ? kScaleUnit * __ldg(p.c.g_v + head) / ll : 0.0f;      // a NaN stays one
 #pragma unroll
         for (int i = 0; i < kDecWarps; ++i) f_s[i][r] *= inv;
         if (p.lse != nullptr) {
           const int tok = static_cast<int>(fast_div(first_row + r, p.group_div));
           p.lse[static_cast<int64_t>(s.r0 + tok) * p.hq + head * p.group + (first_row + r - tok * p.group)] =
-              ll > 0.0f ? (mm - kShift) * kLn2 + logf(ll) : -CUDART_INF_F;
+              ll != 0.0f ? (mm - kShift) * kLn2 + logf(ll) : -CUDART_INF_F;
         }
       } else {
         p.part_ml[static_cast<int64_t>(slot) * kRows + r] = make_float2(mm, ll);
@@ -668,9 +667,9 @@ __global__ void __launch_bounds__(kJoinThreads) attention_combine_kernel(AttnArg
     if (r < R && (!shared || grp == 0)) {
       const int tok = static_cast<int>(fast_div(first_row + r, p.group_div));
       const int64_t row = static_cast<int64_t>(r0 + tok) * p.hq + head * p.group + (first_row + r - tok * p.group);
-      const float inv = l > 0.0f ? kScaleUnit * __ldg(p.c.g_v + head) / l : 0.0f;
+      const float inv = l != 0.0f ? kScaleUnit * __ldg(p.c.g_v + head) / l : 0.0f;
       p.out[row * D + d] = static_cast<uint16_t>(float_to_bf16_bits(o * inv));
-      if (d == 0 && p.lse != nullptr) p.lse[row] = l > 0.0f ? (m - kShift) * kLn2 + logf(l) : -CUDART_INF_F;
+      if (d == 0 && p.lse != nullptr) p.lse[row] = l != 0.0f ? (m - kShift) * kLn2 + logf(l) : -CUDART_INF_F;
     }
     if (shared) __syncthreads();
   }
