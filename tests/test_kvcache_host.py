@@ -39,7 +39,7 @@ def read(l, cache=None, off=P, start=None, table=P, n=2, pages=3, rows=4, k=P, v
     return l.quads_kv_cache_read(cache if cache is not None else desc(), off, start, table, n, pages, rows, k, v, dt, None)
 
 
-def attend(l, cache=None, q=P, rows=4, ld=1024, hq=8, off=P, kv=P, table=P, n=2, pages=3, mq=2, scale=0.1, window=0, out=P,
+def attend(l, cache=None, q=P, rows=4, ld=1024, hq=8, off=P, kv=P, table=P, n=2, pages=3, mq=2, scale=0.1, window=0, out=P << 8,
            lse=None, ws=P, ws_bytes=1 << 40):
     return l.quads_attention_paged(q, rows, ld, hq, cache if cache is not None else desc(), off, kv, table, n, pages, mq, scale,
                                    window, out, lse, ws, ws_bytes, None)
@@ -59,6 +59,7 @@ BAD = [(write, dict(rows=-1)), (write, dict(ld_k=250)), (write, dict(ld_v=128)),
        (attend, dict(kv=None)), (attend, dict(pages=1000, ws=None)), (attend, dict(pages=1000, ws_bytes=100)),
        (attend, dict(pages=1000, ws=P + 4)), (attend, dict(rows=100, mq=50, pages=1000, ws_bytes=100)),
        (attend, dict(n=60000, pages=2000000)), (attend, dict(q=P + 8)), (attend, dict(out=P + 8)),
+       (attend, dict(out=P)), (attend, dict(rows=5, out=P + 2 * (4 * 1024 + 1016))), (attend, dict(out=P - 2 * 4 * 1024 + 16)),
        (rope, dict(T=-1)), (rope, dict(hq=0, hk=0)), (rope, dict(dim=120)), (rope, dict(dim=2048)), (rope, dict(rot=8)),
        (rope, dict(rot=144)), (rope, dict(ld_q=128)), (rope, dict(ldo_k=132)), (rope, dict(q=None)), (rope, dict(ok=None)),
        (rope, dict(pos=None)), (rope, dict(freq=None)), (rope, dict(oq=P + 8))]

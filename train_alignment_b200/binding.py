@@ -853,6 +853,8 @@ def attention_paged(q, cache, row_off, kv_len, block_table, max_q_len, scale=Non
         ws = first.new_empty((need,)) if need else None
     elif ws.get_device() != first.get_device() or not ws.is_contiguous():
         raise ValueError(f"ws must be a contiguous tensor on {first.device}")
+    if max_q_len >> 31 or window >> 31:
+        raise ValueError(f"max_q_len and window must be in [0, 2^31), got {max_q_len} and {window}")
     pw, nw = (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
     _check(lib.quads_attention_paged(q.data_ptr(), rows, ld_q, hq, cache.ref, off, kv, table, n, m, max_q_len,
                                      dim ** -0.5 if scale is None else scale, window, po, pl, pw, nw, stream),

@@ -178,6 +178,9 @@ int quads_attention_paged(const uint16_t* q, int64_t rows, int64_t ld_q, int hea
   const size_t need = quads_attention_paged_workspace_bytes(cache, rows, heads_q, n_seqs, max_pages, max_q_len);
   QUADS_REQUIRE(need == 0 || (ws != nullptr && ws_bytes >= need && aligned(ws, 16)), QUADS_ERR_INVALID_ARG,
                 "a 16-byte aligned workspace of %zu bytes is required", need);
+  const int64_t width = static_cast<int64_t>(heads_q) * cache->head_dim;
+  QUADS_REQUIRE(out + rows * width <= q || q + (rows - 1) * ld_q + width <= out, QUADS_ERR_INVALID_ARG,
+                "out must not overlap q");
   AttnArgs p{};
   p.c = cache_args(cache, block_table, n_seqs, max_pages);
   p.q = q; p.out = out; p.lse = lse; p.off = row_off; p.kv_len = kv_len;
