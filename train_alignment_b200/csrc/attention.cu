@@ -76,9 +76,11 @@ int launch_decode(AttnArgs p, void* ws, int unit_rows, bool whole, cudaStream_t 
   p.by_unit = units <= grid;
   attention_decode_kernel<D, NT, false><<<grid, kDecThreads, 0, stream>>>(p, kDecMinQuota);
   QUADS_TRY(check_launch("attention_decode_kernel"));
-  // rows on blocks of their own where few units are cut into many runs
-  const dim3 join(static_cast<unsigned>(p.by_unit ? units : grid), units * 8 <= grid ? (unit_rows < 8 * NT ? unit_rows : 8 * NT) : 1);
-  QUADS_TRY(launch_dependent(attention_combine_kernel<D, NT>, join, kJoinThreads, stream, "attention_combine_kernel", p));
+  // the join: rows on blocks of their own as far as there are SMs for them
+  const int64_t x = p.by_unit ? units : grid, per = num_sms() / x;
+  const int most = unit_rows < 8 * NT ? unit_rows : 8 * NT;
+  const dim3 join(static_cast<unsigned>(x), static_cast<unsigned>(per < 1 ? 1 : per < most ? per : most));
+  QUADS_TRY(launch_dependent(attention_combine_kernel<D, NT>, join, kJoinThreads * NT, stream, "attention_combine_kernel", p));
   count_launches(2);
   return QUADS_OK;
 }
