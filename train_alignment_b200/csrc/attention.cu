@@ -42,11 +42,16 @@ int launch_dependent(void (*kernel)(Params...), dim3 grid, int threads, cudaStre
 int dec_grid(int nt) { return dec_ctas_per_sm(nt) * num_sms(); }
 // Key tiles (of 128) of a split: shorter ones cost more in joining than they save.
 constexpr int kChMinTiles = 4;
-// Rows of a sequence and key head up to which the kernel for few rows is
-// taken.  16 sequences of up to 8192 keys, 4 key heads: 48 rows 43 us against
-// 60 us in the kernel for many, 32 rows 36 against 60; 64 rows 47 against 60,
-// but at short contexts (64 x 512 keys) 33 against 25.
-constexpr int kDecMaxRows = 48;
+// Whether the kernel for few rows (of a sequence and key head) is taken: up to
+// 48, and up to 64 where the sequences' key heads are no more than the SMs, so
+// that the kernel for many, whose blocks take one each, leaves some idle or
+// waits for the longest.  4 key heads of 128: 16 sequences of up to 8192 keys
+// with 48 rows 35 us against 58, with 64 rows 41 against 58 (of up to 1024
+// keys 15.0 against 16.2); 64 sequences of up to 512 with 64 rows 32 against
+// 24, of up to 2048 60 against 54; 16 of up to 2048 with 96 rows 28 against 23.
+bool few_rows(const quads_kv_cache* c, int n_seqs, int64_t unit_rows) {
+  return unit_rows <= 48 || (unit_rows <= 64 && static_cast<int64_t>(n_seqs) * c->n_heads <= num_sms());
+}
 // Tiles of a run (512 keys): with 2, one context of 65536 takes 21.5 us, most
 // of it joining; with 4, 16.6 us.
 constexpr int kDecMinQuota = 4;
@@ -155,7 +160,7 @@ size_t quads_attention_paged_workspace_bytes(const quads_kv_cache* cache, int64_
   if (cache == nullptr || cache->n_heads < 1 || heads_q < 1 || heads_q % cache->n_heads != 0) return 0;
   if (rows <= 0 || n_seqs <= 0 || max_q_len <= 0 || max_pages < 0) return 0;
   const int64_t unit_rows = static_cast<int64_t>(max_q_len) * (heads_q / cache->n_heads);
-  if (unit_rows <= kDecMaxRows) return dec_whole(cache, max_pages) ? 0 : dec_workspace(cache->head_dim, unit_rows <= 8 ? 1 : 2);
+  if (few_rows(cache, n_seqs, unit_rows)) return dec_whole(cache, max_pages) ? 0 : dec_workspace(cache->head_dim, unit_rows <= 8 ? 1 : 2);
   return chunk_workspace(cache, rows, heads_q, chunk_plan(cache, rows, heads_q, n_seqs, max_pages, max_q_len).n_split);
 }
 
@@ -190,7 +195,7 @@ int quads_attention_paged(const uint16_t* q, int64_t rows, int64_t ld_q, int hea
   p.max_q = max_q_len; p.window = window < (1 << 30) ? window : (1 << 30); p.scale = scale;
   p.group_div = make_fastdiv(static_cast<uint32_t>(p.group));
   const int64_t unit_rows = static_cast<int64_t>(max_q_len) * p.group;
-  if (unit_rows <= kDecMaxRows) {
+  if (few_rows(cache, n_seqs, unit_rows)) {
     const int64_t tiles = (static_cast<int64_t>(max_pages) * cache->page_size / kDecTile + 2) * ceil_div(unit_rows, int64_t(8));
     QUADS_REQUIRE(tiles < (int64_t(1) << 30) && tiles * n_seqs * cache->n_heads < (int64_t(1) << 30),
                   QUADS_ERR_UNSUPPORTED_SHAPE, "too many key tiles: n_seqs * n_heads * (max_pages * page_size / %d + 2) must be below 2^27", kDecTile);
