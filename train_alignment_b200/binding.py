@@ -700,9 +700,9 @@ def _stream(t, name):
     """Raw current stream of t's device, which must be the current one (the
     device the launches go to)."""
     d = t.get_device()
-    if d < 0 or d != torch.cuda.current_device():
-        if d < 0:
-            raise ValueError(f"{name} must be a CUDA tensor")
+    if d < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if d != torch._C._cuda_getDevice():
         raise ValueError(f"{name} is on cuda:{d}, not on the current device cuda:{torch.cuda.current_device()}")
     return torch._C._cuda_getCurrentRawStream(d)
 
@@ -766,14 +766,15 @@ def kv_cache_read(cache, row_off, block_table, rows, start=None, out_dtype=OUT_B
     if out_dtype not in (OUT_BF16, OUT_F32):
         raise ValueError(f"unknown output dtype {out_dtype}")
     dt = torch.bfloat16 if out_dtype == OUT_BF16 else torch.float32
-    shape = (rows, cache.n_heads, cache.head_dim)
+    heads, dim = cache.n_heads, cache.head_dim
+    shape, strides = (rows, heads, dim), (heads * dim, dim, 1)
     if k_out is None:
-        k_out = first.new_empty(shape, dtype=dt)
+        k_out = torch.empty_strided(shape, strides, dtype=dt, device=first.device)
         pk = k_out.data_ptr()
     else:
         pk = _like(k_out, first, dt, shape, "k_out")
     if v_out is None:
-        v_out = first.new_empty(shape, dtype=dt)
+        v_out = torch.empty_strided(shape, strides, dtype=dt, device=first.device)
         pv = v_out.data_ptr()
     else:
         pv = _like(v_out, first, dt, shape, "v_out")
@@ -793,14 +794,14 @@ def _rope(q, k, positions, freq, interleaved, mscale, inverse, q_out, k_out):
         if rows_k != rows or dim_k != dim:
             raise ValueError(f"q and k must have the same rows and head size, got {tuple(q.shape)} and {tuple(k.shape)}")
         if k_out is None:
-            k_out, ld_ko = k.new_empty((rows, hk, dim)), hk * dim
+            k_out, ld_ko = torch.empty_like(k, memory_format=torch.contiguous_format), hk * dim
         else:
             if k_out.shape != k.shape:
                 raise ValueError("k_out must have k's shape")
             ld_ko = _heads_view(k_out, q, "k_out")[3]
         pk, pko = k.data_ptr(), k_out.data_ptr()
     if q_out is None:
-        q_out, ld_qo = q.new_empty((rows, hq, dim)), hq * dim
+        q_out, ld_qo = torch.empty_like(q, memory_format=torch.contiguous_format), hq * dim
     else:
         if q_out.shape != q.shape:
             raise ValueError("q_out must have q's shape")
@@ -842,7 +843,7 @@ def attention_paged(q, cache, row_off, kv_len, block_table, max_q_len, scale=Non
     n, m, off, table = _tables(cache, row_off, block_table)
     kv = _like(kv_len, first, torch.int32, (n,), "kv_len")
     if out is None:
-        out = q.new_empty((rows, hq, dim))
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
         po = out.data_ptr()
     else:
         po = _like(out, first, torch.bfloat16, (rows, hq, dim), "out")
