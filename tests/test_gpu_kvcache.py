@@ -251,10 +251,10 @@ def test_rows_in_groups(cuda_lib, dim, heads, group, new, kv):
     _attend(heads, group, dim, 48, new, kv, window=130, seed=37, garbage=True)
 
 
-@pytest.mark.parametrize("heads,n", [(1, 200), (4, 200), (8, 129)])
-def test_many_sequences(cuda_lib, heads, n):
+@pytest.mark.parametrize("heads,n,longest", [(1, 200, 1500), (4, 200, 1500), (8, 129, 1500), (4, 200, 1000)])
+def test_many_sequences(cuda_lib, heads, n, longest):
     """More sequences than one scan takes; units by themselves and by the CTA that begins them; sequences without rows."""
-    kv = [1 + (37 * b) % 1500 for b in range(n)]
+    kv = [1 + (37 * b) % longest for b in range(n)]
     new = [0 if b % 7 == 3 else 1 + b % 3 for b in range(n)]
     _attend(heads, 4, 64, 16, new, [max(k, m) for k, m in zip(kv, new)], seed=38)
 

@@ -52,24 +52,39 @@ constexpr int kChMinTiles = 4;
 bool few_rows(const quads_kv_cache* c, int n_seqs, int64_t unit_rows) {
   return unit_rows <= 48 || (unit_rows <= 64 && static_cast<int64_t>(n_seqs) * c->n_heads <= num_sms());
 }
-// Tiles of a run (512 keys): with 2, one context of 65536 takes 21.5 us, most
-// of it joining; with 4, 16.6 us.
-constexpr int kDecMinQuota = 4;
+// Tiles of a run, at least: as few as leave a unit at most 192 parts to join
+// (one key head's 65536 keys: 171 parts 12.0 us, 256 13.2, 128 12.4).  Four
+// contexts of 2048: runs of 1 tile 9.6 us, of 4 11.8.
+constexpr int kDecMaxParts = 192;
 
 size_t dec_workspace(int D, int nt) {
   return static_cast<size_t>(dec_grid(nt)) * (2 * (8 * nt) * (D * sizeof(float) + sizeof(float2)) + sizeof(int4));
 }
 
-// One CTA per unit where no context is longer than kDecWhole tiles.
-bool dec_whole(const quads_kv_cache* c, int max_pages) {
-  return static_cast<int64_t>(max_pages) * c->page_size <= kDecWhole * kDecTile;
+// Keys that a unit can see, at most.
+int64_t dec_keys(const quads_kv_cache* c, int max_pages, int max_q_len, int window) {
+  const int64_t all = static_cast<int64_t>(max_pages) * c->page_size, seen = static_cast<int64_t>(window) + max_q_len + 15;
+  return window > 0 && seen < all ? seen : all;
+}
+int64_t dec_units(const quads_kv_cache* c, int n_seqs, int64_t unit_rows) {
+  return static_cast<int64_t>(n_seqs) * c->n_heads * ceil_div(unit_rows, int64_t(unit_rows <= 8 ? 8 : 16));
+}
+
+// Whether a CTA takes whole units: contexts of at most 5 tiles (32 units of
+// 600 keys: 7.2 us, cut into tiles and joined 7.8), and of at most 8 where the
+// units fill the SMs well enough (96 units of 1024: 9.6 against 11.2; 64: 9.7
+// against 9.0, 8: 9.4 against 7.4).
+bool dec_whole(const quads_kv_cache* c, int64_t keys, int n_seqs, int64_t unit_rows) {
+  return keys <= 5 * kDecTile ||
+         (keys <= 8 * kDecTile && 6 * dec_units(c, n_seqs, unit_rows) > dec_grid(unit_rows <= 8 ? 1 : 2));
 }
 
 template <int D, int NT>
-int launch_decode(AttnArgs p, void* ws, int unit_rows, bool whole, cudaStream_t stream) {
+int launch_decode(AttnArgs p, void* ws, int unit_rows, int64_t keys, bool whole, cudaStream_t stream) {
   const int grid = dec_grid(NT);
   p.row_groups = (unit_rows + 8 * NT - 1) / (8 * NT);
   const int64_t units = static_cast<int64_t>(p.c.n_seqs) * p.c.n_heads * p.row_groups;
+  const int64_t tiles = ceil_div(keys, int64_t(kDecTile));
   if (whole) {
     attention_decode_kernel<D, NT, true><<<static_cast<unsigned>(units < grid ? units : grid), kDecThreads, 0, stream>>>(p, 0);
     count_launches(1);
@@ -79,7 +94,7 @@ int launch_decode(AttnArgs p, void* ws, int unit_rows, bool whole, cudaStream_t 
   p.part_o = reinterpret_cast<float*>(p.cuts + grid);
   p.part_ml = reinterpret_cast<float2*>(p.part_o + static_cast<size_t>(2) * grid * (8 * NT) * D);
   p.by_unit = units <= grid;
-  attention_decode_kernel<D, NT, false><<<grid, kDecThreads, 0, stream>>>(p, kDecMinQuota);
+  attention_decode_kernel<D, NT, false><<<grid, kDecThreads, 0, stream>>>(p, static_cast<int>(ceil_div(tiles, int64_t(kDecMaxParts))));
   QUADS_TRY(check_launch("attention_decode_kernel"));
   // the join: rows on blocks of their own as far as there are SMs for them
   const int64_t x = p.by_unit ? units : grid, per = num_sms() / x;
@@ -160,7 +175,10 @@ size_t quads_attention_paged_workspace_bytes(const quads_kv_cache* cache, int64_
   if (cache == nullptr || cache->n_heads < 1 || heads_q < 1 || heads_q % cache->n_heads != 0) return 0;
   if (rows <= 0 || n_seqs <= 0 || max_q_len <= 0 || max_pages < 0) return 0;
   const int64_t unit_rows = static_cast<int64_t>(max_q_len) * (heads_q / cache->n_heads);
-  if (few_rows(cache, n_seqs, unit_rows)) return dec_whole(cache, max_pages) ? 0 : dec_workspace(cache->head_dim, unit_rows <= 8 ? 1 : 2);
+  if (few_rows(cache, n_seqs, unit_rows)) {               // without a window, with which a call may need none
+    const int64_t keys = dec_keys(cache, max_pages, max_q_len, 0);
+    return dec_whole(cache, keys, n_seqs, unit_rows) ? 0 : dec_workspace(cache->head_dim, unit_rows <= 8 ? 1 : 2);
+  }
   return chunk_workspace(cache, rows, heads_q, chunk_plan(cache, rows, heads_q, n_seqs, max_pages, max_q_len).n_split);
 }
 
@@ -200,10 +218,11 @@ int quads_attention_paged(const uint16_t* q, int64_t rows, int64_t ld_q, int hea
     QUADS_REQUIRE(tiles < (int64_t(1) << 30) && tiles * n_seqs * cache->n_heads < (int64_t(1) << 30),
                   QUADS_ERR_UNSUPPORTED_SHAPE, "too many key tiles: n_seqs * n_heads * (max_pages * page_size / %d + 2) must be below 2^27", kDecTile);
     const int n = static_cast<int>(unit_rows);
-    const bool whole = dec_whole(cache, max_pages);
+    const int64_t keys = dec_keys(cache, max_pages, max_q_len, window);
+    const bool whole = dec_whole(cache, keys, n_seqs, unit_rows);
     if (cache->head_dim == 64)
-      return n <= 8 ? launch_decode<64, 1>(p, ws, n, whole, stream) : launch_decode<64, 2>(p, ws, n, whole, stream);
-    return n <= 8 ? launch_decode<128, 1>(p, ws, n, whole, stream) : launch_decode<128, 2>(p, ws, n, whole, stream);
+      return n <= 8 ? launch_decode<64, 1>(p, ws, n, keys, whole, stream) : launch_decode<64, 2>(p, ws, n, keys, whole, stream);
+    return n <= 8 ? launch_decode<128, 1>(p, ws, n, keys, whole, stream) : launch_decode<128, 2>(p, ws, n, keys, whole, stream);
   }
   const ChunkPlan plan = chunk_plan(cache, rows, heads_q, n_seqs, max_pages, max_q_len);
   QUADS_REQUIRE(plan.blocks * cache->n_heads < (int64_t(1) << 31) && ceil_div(rows * heads_q, int64_t(8)) < (int64_t(1) << 31),

@@ -5,9 +5,8 @@
 // tiles of 128, and the tiles of all units, end to end, into equal runs, one
 // per CTA, so that sequences of any lengths load the SMs alike.  A unit that
 // several CTAs share leaves partial sums that attention_combine_kernel joins
-// in order.  Where no context is longer than kDecWhole tiles a CTA takes whole
-// units and nothing is joined: 700 keys in one launch instead of two, 8.5 us
-// against 12.
+// in order.  Where contexts are short a CTA takes whole units and nothing is
+// joined (one launch instead of two).
 //
 // A CTA's four warps take 32 keys each of a tile, from a ring in shared memory
 // (cp.async, the next step's copies under this one's arithmetic) into the
@@ -42,7 +41,6 @@ constexpr int kDecThreads = 128;
 constexpr int kDecWarps = kDecThreads / 32;
 constexpr int kDecSub = 2;                            // groups of 16 keys of a warp's step
 constexpr int kDecTile = 16 * kDecSub * kDecWarps;
-constexpr int kDecWhole = 8;                          // tiles of a context that is not cut
 // Resident CTAs of an SM: its registers hold 168 (255) a thread.  Four of 128
 // (three of 168) are within 5 % at 8 rows and up to 40 % slower at 16.
 __host__ __device__ constexpr int dec_ctas_per_sm(int nt) { return nt == 1 ? 3 : 2; }
