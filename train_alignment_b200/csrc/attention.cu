@@ -56,6 +56,14 @@ bool few_rows(const quads_kv_cache* c, int n_seqs, int64_t unit_rows) {
 // (one key head's 65536 keys: 171 parts 12.0 us, 256 13.2, 128 12.4).  Four
 // contexts of 2048: runs of 1 tile 9.6 us, of 4 11.8.
 constexpr int kDecMaxParts = 192;
+// What beginning and ending a unit costs, in tiles: runs are equal with it, so
+// that one with two ends in it has fewer tiles.  A run's tile takes about
+// 1.4 us (three share an SM), its look-ups, fill and join 2.4 or more: without
+// it the runs of 64 contexts of up to 4096 ended at 18.2, 20.8 and 22.8 us by
+// the units in them.  0, 1, 2, 3, 4: 27.1, 25.7, 26.1, 25.5, 26.9 us (whole
+// tiles); 256 contexts of up to 2000 99, 92, 89, 86, 87.  Not where a run would
+// have but a tile or two.
+constexpr int kDecUnitCost = 3;
 
 size_t dec_workspace(int D, int nt) {
   return static_cast<size_t>(dec_grid(nt)) * (2 * (8 * nt) * (D * sizeof(float) + sizeof(float2)) + sizeof(int4));
@@ -94,6 +102,7 @@ int launch_decode(AttnArgs p, void* ws, int unit_rows, int64_t keys, bool whole,
   p.part_o = reinterpret_cast<float*>(p.cuts + grid);
   p.part_ml = reinterpret_cast<float2*>(p.part_o + static_cast<size_t>(2) * grid * (8 * NT) * D);
   p.by_unit = units <= grid;
+  p.unit_cost = units * tiles >= 2 * grid ? kDecUnitCost : 0;
   attention_decode_kernel<D, NT, false><<<grid, kDecThreads, 0, stream>>>(p, static_cast<int>(ceil_div(tiles, int64_t(kDecMaxParts))));
   QUADS_TRY(check_launch("attention_decode_kernel"));
   // the join: rows on blocks of their own as far as there are SMs for them
@@ -214,9 +223,9 @@ int quads_attention_paged(const uint16_t* q, int64_t rows, int64_t ld_q, int hea
   p.group_div = make_fastdiv(static_cast<uint32_t>(p.group));
   const int64_t unit_rows = static_cast<int64_t>(max_q_len) * p.group;
   if (few_rows(cache, n_seqs, unit_rows)) {
-    const int64_t tiles = (static_cast<int64_t>(max_pages) * cache->page_size / kDecTile + 2) * ceil_div(unit_rows, int64_t(8));
+    const int64_t tiles = (static_cast<int64_t>(max_pages) * cache->page_size / kDecTile + 2 + kDecUnitCost) * ceil_div(unit_rows, int64_t(8));
     QUADS_REQUIRE(tiles < (int64_t(1) << 30) && tiles * n_seqs * cache->n_heads < (int64_t(1) << 30),
-                  QUADS_ERR_UNSUPPORTED_SHAPE, "too many key tiles: n_seqs * n_heads * (max_pages * page_size / %d + 2) must be below 2^27", kDecTile);
+                  QUADS_ERR_UNSUPPORTED_SHAPE, "too many key tiles: n_seqs * n_heads * (max_pages * page_size / %d + %d) must be below 2^27", kDecTile, 2 + kDecUnitCost);
     const int n = static_cast<int>(unit_rows);
     const int64_t keys = dec_keys(cache, max_pages, max_q_len, window);
     const bool whole = dec_whole(cache, keys, n_seqs, unit_rows);

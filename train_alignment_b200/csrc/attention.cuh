@@ -28,6 +28,7 @@ struct AttnArgs {
   int4* cuts;
   int by_unit;
   int row_groups;           // units of a sequence and key head, at most
+  int unit_cost;            // what beginning and ending a unit costs, in key tiles
 };
 
 // A sequence of a call: its rows, and the keys that they can see.

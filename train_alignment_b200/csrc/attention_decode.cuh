@@ -3,10 +3,11 @@
 //
 // A unit is (sequence, key head, 8 NT of its rows); its keys are cut into
 // tiles of 128, and the tiles of all units, end to end, into equal runs, one
-// per CTA, so that sequences of any lengths load the SMs alike.  A unit that
-// several CTAs share leaves partial sums that attention_combine_kernel joins
-// in order.  Where contexts are short a CTA takes whole units and nothing is
-// joined (one launch instead of two).
+// per CTA, so that sequences of any lengths load the SMs alike; a unit's tiles
+// come after a few slots that stand for what beginning and ending it costs.  A
+// unit that several CTAs share leaves partial sums that
+// attention_combine_kernel joins in order.  Where contexts are short a CTA
+// takes whole units and nothing is joined (one launch instead of two).
 //
 // A CTA's four warps take 32 keys each of a tile, from a ring in shared memory
 // (cp.async, the next step's copies under this one's arithmetic) into the
@@ -55,8 +56,8 @@ __device__ __forceinline__ int dec_groups(const AttnArgs& p, const SeqInfo& s) {
   return (max(s.nq, 0) * p.group + kRows - 1) / kRows;
 }
 
-// The run of this CTA: tiles [w0, w1) of all units' (fewer than 2^30, checked
-// on the host), and the sequence of the first with the first tile of its first
+// The run of this CTA: slots [w0, w1) of all units' (fewer than 2^30, checked
+// on the host), and the sequence of the first with the first slot of its first
 // unit.  Calls of up to kDecThreads sequences scan them once and keep them.
 template <int kRows>
 struct DecPlan {
@@ -64,7 +65,7 @@ struct DecPlan {
   int b, base;
   SeqInfo seq[kDecThreads];
 
-  // tiles (of one head's units) of sequences c0 .. c0 + kDecThreads - 1: this
+  // slots (of one head's units) of sequences c0 .. c0 + kDecThreads - 1: this
   // thread's, those before it, and all
   __device__ __forceinline__ int scan(const AttnArgs& p, int c0, int& before, int& n) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, i = c0 + threadIdx.x;
@@ -72,7 +73,7 @@ struct DecPlan {
     if (i < p.c.n_seqs) {
       const SeqInfo s = seq_info(p, i);
       const int groups = dec_groups<kRows>(p, s);
-      n = dec_tiles(s) * groups;
+      n = (dec_tiles(s) + p.unit_cost) * groups;
       seq[threadIdx.x] = s;
       if (p.by_unit && blockIdx.x == 0)                 // units that this sequence has not
         for (int h = 0; h < p.c.n_heads; ++h)
@@ -248,7 +249,7 @@ __global__ void __launch_bounds__(kDecThreads, dec_ctas_per_sm(NT)) attention_de
 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
-  // a run of tiles [w0, w1), or (kWhole) units blockIdx.x, + gridDim.x, ...
+  // a run of slots [w0, w1), or (kWhole) units blockIdx.x, + gridDim.x, ...
   int quota = 1, w0 = blockIdx.x, w1 = p.c.n_seqs * p.c.n_heads * p.row_groups, b = 0, base = 0;
   bool told = false;                                    // thread 0: this run's cut is written
   if constexpr (!kWhole) {
@@ -262,7 +263,8 @@ __global__ void __launch_bounds__(kDecThreads, dec_ctas_per_sm(NT)) attention_de
 
   for (int w = w0; w < w1;) {
     SeqInfo s;
-    int nt, head, grp, tile0, tile1;                    // grp: which 8 NT of the rows
+    int nt, head, grp, tile0, tile1, next;              // grp: which 8 NT of the rows
+    int left = 0;                                       // slots of the unit from w on
     if constexpr (kWhole) {
       const int bh = static_cast<int>(static_cast<unsigned>(w) / static_cast<unsigned>(p.row_groups));
       grp = w - bh * p.row_groups;
@@ -272,25 +274,29 @@ __global__ void __launch_bounds__(kDecThreads, dec_ctas_per_sm(NT)) attention_de
       nt = dec_tiles(s);
       tile0 = 0;
       tile1 = nt;
+      next = w + static_cast<int>(gridDim.x);
       if (grp >= dec_groups<kRows>(p, s)) {
-        w += gridDim.x;
+        w = next;
         continue;
       }
     } else {
       s = plan.info(p, b);
       nt = dec_tiles(s);
-      int per_head = nt * dec_groups<kRows>(p, s);
+      int per_head = (nt + p.unit_cost) * dec_groups<kRows>(p, s);
       while (w >= base + per_head * p.c.n_heads) {      // on to the next sequence with rows
         base += per_head * p.c.n_heads;
         s = plan.info(p, ++b);
         nt = dec_tiles(s);
-        per_head = nt * dec_groups<kRows>(p, s);
+        per_head = (nt + p.unit_cost) * dec_groups<kRows>(p, s);
       }
       head = static_cast<int>(static_cast<unsigned>(w - base) / static_cast<unsigned>(per_head));
       const int rest = w - base - head * per_head;
-      grp = static_cast<int>(static_cast<unsigned>(rest) / static_cast<unsigned>(nt));
-      tile0 = rest - grp * nt;
-      tile1 = min(nt, tile0 + (w1 - w));
+      grp = static_cast<int>(static_cast<unsigned>(rest) / static_cast<unsigned>(nt + p.unit_cost));
+      left = nt + p.unit_cost - (rest - grp * (nt + p.unit_cost));
+      tile0 = max(nt - left, 0);
+      tile1 = nt - max(left - (w1 - w), 0);
+      next = w + min(left, w1 - w);
+      if (tile1 <= 0) break;                            // the run ends before the unit's first tile
     }
     const int first_row = grp * kRows;
     const int R = min(s.nq * p.group - first_row, kRows);
@@ -555,7 +561,7 @@ __global__ void __launch_bounds__(kDecThreads, dec_ctas_per_sm(NT)) attention_de
     const bool whole = kWhole || (tile0 == 0 && tile1 == nt);
     // the run that begins a unit says whether and where others go on with it
     if (!kWhole && tile0 == 0 && threadIdx.x == 0) {
-      const int last = static_cast<int>(static_cast<unsigned>(w + nt - 1) / static_cast<unsigned>(quota));
+      const int last = static_cast<int>(static_cast<unsigned>(w + left - 1) / static_cast<unsigned>(quota));
       const int4 cut = make_int4(whole ? -1 : slot, last, s.r0 * p.c.n_heads + head, R | (first_row << 8));
       if (p.by_unit)
         p.cuts[(b * p.c.n_heads + head) * p.row_groups + grp] = cut;
@@ -606,7 +612,7 @@ __global__ void __launch_bounds__(kDecThreads, dec_ctas_per_sm(NT)) attention_de
       }
     }
     __syncthreads();
-    w += kWhole ? static_cast<int>(gridDim.x) : tile1 - tile0;
+    w = next;
   }
   if (!kWhole && !p.by_unit && threadIdx.x == 0 && !told) p.cuts[blockIdx.x] = make_int4(-1, 0, 0, 0);
 }
