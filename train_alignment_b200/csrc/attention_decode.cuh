@@ -63,6 +63,7 @@ template <int kRows>
 struct DecPlan {
   int warp_s[kDecWarps];
   int b, base;
+  int quota, longer;       // slots of a run; the first so many runs have one more
   SeqInfo seq[kDecThreads];
 
   // slots (of one head's units) of sequences c0 .. c0 + kDecThreads - 1: this
@@ -99,18 +100,25 @@ struct DecPlan {
   }
 
   // false: nothing to do
-  __device__ __forceinline__ bool run(const AttnArgs& p, int min_quota, int& quota, int& w0, int& w1) {
+  __device__ __forceinline__ bool run(const AttnArgs& p, int min_quota, int& w0, int& w1) {
     int before, n, all = 0;
     for (int c0 = 0; c0 < p.c.n_seqs; c0 += kDecThreads) {
       if (c0) __syncthreads();
       all += scan(p, c0, before, n);
     }
     const int total = all * p.c.n_heads;
-    quota = max(static_cast<int>(static_cast<unsigned>(total + gridDim.x - 1) / gridDim.x), min_quota);
-    const int64_t first = static_cast<int64_t>(quota) * blockIdx.x;
-    if (first >= total) return false;
-    w0 = static_cast<int>(first);
-    w1 = min(total, w0 + quota);
+    unsigned runs = static_cast<unsigned>(total);
+    if (min_quota > 1) runs = (runs + min_quota - 1) / static_cast<unsigned>(min_quota);
+    runs = min(runs, gridDim.x);
+    if (blockIdx.x >= runs) return false;
+    const int i = static_cast<int>(blockIdx.x), q = static_cast<int>(static_cast<unsigned>(total) / runs);
+    const int more = total - q * static_cast<int>(runs);
+    w0 = q * i + min(i, more);
+    w1 = w0 + q + (i < more ? 1 : 0);
+    if (threadIdx.x == 0) {
+      quota = q;
+      longer = more;
+    }
     int run = 0;
     for (int c0 = 0;; c0 += kDecThreads) {
       if (p.c.n_seqs > kDecThreads) {
@@ -127,6 +135,12 @@ struct DecPlan {
     }
     __syncthreads();
     return true;
+  }
+  // the run of a slot
+  __device__ __forceinline__ int run_of(int w) const {
+    const int far = longer * (quota + 1);
+    return w < far ? static_cast<int>(static_cast<unsigned>(w) / static_cast<unsigned>(quota + 1))
+                   : longer + static_cast<int>(static_cast<unsigned>(w - far) / static_cast<unsigned>(quota));
   }
   __device__ __forceinline__ SeqInfo info(const AttnArgs& p, int i) const {
     return p.c.n_seqs <= kDecThreads ? seq[i] : seq_info(p, i);
@@ -250,10 +264,10 @@ __global__ void __launch_bounds__(kDecThreads, dec_ctas_per_sm(NT)) attention_de
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t = lane & 3;
   // a run of slots [w0, w1), or (kWhole) units blockIdx.x, + gridDim.x, ...
-  int quota = 1, w0 = blockIdx.x, w1 = p.c.n_seqs * p.c.n_heads * p.row_groups, b = 0, base = 0;
+  int w0 = blockIdx.x, w1 = p.c.n_seqs * p.c.n_heads * p.row_groups, b = 0, base = 0;
   bool told = false;                                    // thread 0: this run's cut is written
   if constexpr (!kWhole) {
-    if (!plan.run(p, min_quota, quota, w0, w1)) {
+    if (!plan.run(p, min_quota, w0, w1)) {
       if (!p.by_unit && threadIdx.x == 0) p.cuts[blockIdx.x] = make_int4(-1, 0, 0, 0);
       return;
     }
@@ -561,8 +575,7 @@ __global__ void __launch_bounds__(kDecThreads, dec_ctas_per_sm(NT)) attention_de
     const bool whole = kWhole || (tile0 == 0 && tile1 == nt);
     // the run that begins a unit says whether and where others go on with it
     if (!kWhole && tile0 == 0 && threadIdx.x == 0) {
-      const int last = static_cast<int>(static_cast<unsigned>(w + left - 1) / static_cast<unsigned>(quota));
-      const int4 cut = make_int4(whole ? -1 : slot, last, s.r0 * p.c.n_heads + head, R | (first_row << 8));
+      const int4 cut = make_int4(whole ? -1 : slot, plan.run_of(w + left - 1), s.r0 * p.c.n_heads + head, R | (first_row << 8));
       if (p.by_unit)
         p.cuts[(b * p.c.n_heads + head) * p.row_groups + grp] = cut;
       else if (!whole)
