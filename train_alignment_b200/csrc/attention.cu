@@ -74,18 +74,13 @@ int64_t dec_keys(const quads_kv_cache* c, int max_pages, int max_q_len, int wind
   const int64_t all = static_cast<int64_t>(max_pages) * c->page_size, seen = static_cast<int64_t>(window) + max_q_len + 15;
   return window > 0 && seen < all ? seen : all;
 }
-int64_t dec_units(const quads_kv_cache* c, int n_seqs, int64_t unit_rows) {
-  return static_cast<int64_t>(n_seqs) * c->n_heads * ceil_div(unit_rows, int64_t(unit_rows <= 8 ? 8 : 16));
-}
-
-// Whether a CTA takes whole units: contexts of at most 5 tiles (32 units of
-// 600 keys: 7.2 us, cut into tiles and joined 7.8), and of at most 8 where the
-// units fill the SMs well enough (96 units of 1024: 9.6 against 11.2; 64: 9.7
-// against 9.0, 8: 9.4 against 7.4).
-bool dec_whole(const quads_kv_cache* c, int64_t keys, int n_seqs, int64_t unit_rows) {
-  return keys <= 5 * kDecTile ||
-         (keys <= 8 * kDecTile && 6 * dec_units(c, n_seqs, unit_rows) > dec_grid(unit_rows <= 8 ? 1 : 2));
-}
+// Whether a CTA takes whole units: contexts of at most 8 tiles.  64 contexts of
+// up to 1024, 8 heads: 19.3 us in one launch, 23.9 cut and joined in two; one
+// context of 700, 4 heads: 8.2 us on the GPU against 6.9, but called one by
+// one 15.3 against 19.8, because the host's second launch and workspace cost
+// more than that.
+constexpr int kDecWhole = 8;
+bool dec_whole(int64_t keys) { return keys <= kDecWhole * kDecTile; }
 
 template <int D, int NT>
 int launch_decode(AttnArgs p, void* ws, int unit_rows, int64_t keys, bool whole, cudaStream_t stream) {
@@ -186,7 +181,7 @@ size_t quads_attention_paged_workspace_bytes(const quads_kv_cache* cache, int64_
   const int64_t unit_rows = static_cast<int64_t>(max_q_len) * (heads_q / cache->n_heads);
   if (few_rows(cache, n_seqs, unit_rows)) {               // without a window, with which a call may need none
     const int64_t keys = dec_keys(cache, max_pages, max_q_len, 0);
-    return dec_whole(cache, keys, n_seqs, unit_rows) ? 0 : dec_workspace(cache->head_dim, unit_rows <= 8 ? 1 : 2);
+    return dec_whole(keys) ? 0 : dec_workspace(cache->head_dim, unit_rows <= 8 ? 1 : 2);
   }
   return chunk_workspace(cache, rows, heads_q, chunk_plan(cache, rows, heads_q, n_seqs, max_pages, max_q_len).n_split);
 }
@@ -228,7 +223,7 @@ int quads_attention_paged(const uint16_t* q, int64_t rows, int64_t ld_q, int hea
                   QUADS_ERR_UNSUPPORTED_SHAPE, "too many key tiles: n_seqs * n_heads * (max_pages * page_size / %d + %d) must be below 2^27", kDecTile, 2 + kDecUnitCost);
     const int n = static_cast<int>(unit_rows);
     const int64_t keys = dec_keys(cache, max_pages, max_q_len, window);
-    const bool whole = dec_whole(cache, keys, n_seqs, unit_rows);
+    const bool whole = dec_whole(keys);
     if (cache->head_dim == 64)
       return n <= 8 ? launch_decode<64, 1>(p, ws, n, keys, whole, stream) : launch_decode<64, 2>(p, ws, n, keys, whole, stream);
     return n <= 8 ? launch_decode<128, 1>(p, ws, n, keys, whole, stream) : launch_decode<128, 2>(p, ws, n, keys, whole, stream);
