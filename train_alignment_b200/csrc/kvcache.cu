@@ -121,7 +121,7 @@ __device__ __forceinline__ Block block_of(const BlockMap& m, int i) {
 // --------------------------------------------------------------- the write
 // One thread per block of 16 elements: 32 bytes in (one access where the rows
 // are 32-byte aligned), 8 + 1 bytes out.  Bound by HBM: 2 bytes read and
-// 0.5625 written per element.  16493 tokens of 8 heads of 128 (87 MB): 21 us,
+// 0.5625 written per element.  16493 tokens of 8 heads of 128 (87 MB): 19 us,
 // three quarters of the issue slots taken.
 template <bool kWide>
 __global__ void __launch_bounds__(kThreads) kv_write_kernel(CacheArgs c, const uint16_t* __restrict__ k,
