@@ -244,7 +244,8 @@ def test_chunks(cuda_lib, dim, heads, group, new, kv):
 @pytest.mark.parametrize("heads,group,new,kv", [
     (2, 4, [3, 8, 12, 1, 0, 5], [300, 2000, 1100, 1500, 40, 5]), (1, 16, [3, 1, 2], [4000, 1100, 1025]),
     (1, 1, [48, 17, 33], [48, 900, 2000]), (3, 6, [8, 3], [8, 1300]), (1, 48, [1, 0, 1], [2100, 0, 700]),
-    (2, 8, [8, 0, 7, 1], [3000, 0, 1100, 40]), (1, 64, [1, 1], [5000, 17])])
+    (2, 8, [8, 0, 7, 1], [3000, 0, 1100, 40]), (1, 64, [1, 1], [5000, 17]),
+    (4, 4, [16, 9] + [1, 0, 3] * 13, [1500, 300] + [30, 0, 200] * 13)])
 def test_rows_in_groups(cuda_lib, dim, heads, group, new, kv):
     """17 to 64 rows of a key head: several units, of which a sequence may have fewer."""
     _attend(heads, group, dim, 16, new, kv, seed=36, extra=1, garbage=True)

@@ -1,5 +1,4 @@
 """Refusals of the KV cache's entry points, on the host: no launch is made."""
-import ctypes
 import math
 
 import pytest
@@ -22,8 +21,8 @@ def lib():
 def desc(**kw):
     d = dict(n_pages=8, page_size=16, n_heads=2, head_dim=128, k_codes=P, k_scales=P, v_codes=P, v_scales=P, g_k=P, g_v=P)
     d.update(kw)
-    return ctypes.byref(B.KVCacheDesc(d["n_pages"], d["page_size"], d["n_heads"], d["head_dim"], 0, d["k_codes"], d["k_scales"],
-                                      d["v_codes"], d["v_scales"], d["g_k"], d["g_v"]))
+    return B.kv_cache_desc(d["n_pages"], d["page_size"], d["n_heads"], d["head_dim"], 0,
+                           *(d[n] or 0 for n in ("k_codes", "k_scales", "v_codes", "v_scales", "g_k", "g_v")))
 
 
 BAD_CACHES = [dict(n_pages=-1), dict(n_pages=1 << 31), dict(page_size=0), dict(page_size=24), dict(page_size=1 << 17),

@@ -6,7 +6,6 @@ and the KV cache in FP4.  KVCache holds the pages and their decode scales; it
 is written with binding.kv_cache_write, attended with
 binding.attention_paged and read back with binding.kv_cache_read.
 """
-import ctypes
 import math
 
 import torch
@@ -42,9 +41,8 @@ class KVCache:
         self.n_pages, self.n_heads, self.page_size, self.head_dim = n_pages, n_heads, page_size, 2 * half
         self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
         self.g_k, self.g_v = g_k, g_v
-        self.desc = B.KVCacheDesc(n_pages, page_size, n_heads, 2 * half, 0, k_codes.data_ptr(), k_scales.data_ptr(),
-                                  v_codes.data_ptr(), v_scales.data_ptr(), g_k.data_ptr(), g_v.data_ptr())
-        self.ref = ctypes.byref(self.desc)
+        self.desc = B.kv_cache_desc(n_pages, page_size, n_heads, 2 * half, 0, k_codes.data_ptr(), k_scales.data_ptr(),
+                                    v_codes.data_ptr(), v_scales.data_ptr(), g_k.data_ptr(), g_v.data_ptr())
 
     @classmethod
     def empty(cls, n_pages, page_size, n_heads, head_dim, amax_k, amax_v, device="cuda"):
