@@ -671,6 +671,7 @@ int quads_rope(const uint16_t* q, int64_t ld_q, int heads_q, const uint16_t* k, 
  *             is a multiple of n_heads.  out must not overlap q.
  *   max_q_len at least the rows of the longest sequence (a longer sequence's
  *             rows past it are not computed); the work is laid out by it.
+ *   max_pages at most (2^31 - 2^16) / page_size.
  *   lse       (nullable) device float [rows][heads_q]: log sum_j exp(scale
  *             q . k_j), -inf for a row of zeros.
  *   ws        device workspace of quads_attention_paged_workspace_bytes()

@@ -58,7 +58,7 @@ BAD = [(write, dict(rows=-1)), (write, dict(ld_k=250)), (write, dict(ld_v=128)),
        (attend, dict(kv=None)), (attend, dict(pages=1000, ws=None)), (attend, dict(pages=1000, ws_bytes=100)),
        (attend, dict(pages=1000, ws=P + 4)), (attend, dict(rows=100, mq=50, pages=1000, ws_bytes=100)),
        (attend, dict(n=60000, pages=2000000)), (attend, dict(q=P + 8)), (attend, dict(out=P + 8)),
-       (attend, dict(out=P)), (attend, dict(rows=5, out=P + 2 * (4 * 1024 + 1016))), (attend, dict(out=P - 2 * 4 * 1024 + 16)),
+       (attend, dict(pages=(1 << 27) - (1 << 12) + 1)), (attend, dict(out=P)), (attend, dict(rows=5, out=P + 2 * (4 * 1024 + 1016))), (attend, dict(out=P - 2 * 4 * 1024 + 16)),
        (rope, dict(T=-1)), (rope, dict(hq=0, hk=0)), (rope, dict(dim=120)), (rope, dict(dim=2048)), (rope, dict(rot=8)),
        (rope, dict(rot=144)), (rope, dict(ld_q=128)), (rope, dict(ldo_k=132)), (rope, dict(q=None)), (rope, dict(ok=None)),
        (rope, dict(pos=None)), (rope, dict(freq=None)), (rope, dict(oq=P + 8))]

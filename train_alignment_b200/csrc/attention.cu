@@ -199,6 +199,9 @@ int quads_attention_paged(const uint16_t* q, int64_t rows, int64_t ld_q, int hea
                 "heads_q (%d) must be a multiple of the cache's %d heads, at most 4096", heads_q, cache->n_heads);
   QUADS_REQUIRE(ld_q >= static_cast<int64_t>(heads_q) * cache->head_dim && ld_q % 8 == 0, QUADS_ERR_INVALID_ARG,
                 "q's row stride must be a multiple of 8 of at least heads_q * head_dim");
+  // positions of a tile's keys then fit 32 bits
+  QUADS_REQUIRE(static_cast<int64_t>(max_pages) * cache->page_size <= (int64_t(1) << 31) - (1 << 16),
+                QUADS_ERR_UNSUPPORTED_SHAPE, "max_pages * page_size must be at most 2^31 - 2^16");
   QUADS_REQUIRE(window >= 0 && max_q_len >= 0, QUADS_ERR_INVALID_ARG, "window and max_q_len must be >= 0");
   QUADS_REQUIRE(scale - scale == 0.0f, QUADS_ERR_INVALID_ARG, "the scale must be finite");
   if (rows == 0 || n_seqs == 0 || max_q_len == 0) return QUADS_OK;
