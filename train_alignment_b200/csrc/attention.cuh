@@ -97,7 +97,8 @@ __device__ __forceinline__ uint32_t scale_pair_f16x2(uint32_t s0, uint32_t s1) {
 constexpr float kScaleUnit = 256.0f;      // what the 2^-8 above is undone with
 
 constexpr uint32_t kNoRow = 0xFFFFFFFFu;     // in place of a cache row: no page
-constexpr float kNoMax = -1e30f;             // the running maximum before the first key: finite, so that
+constexpr float kNoMax = -3.402823466e38f;   // the running maximum before the first key: the lowest finite
+                                             // number, so that no finite score is below it and
                                              // differences of maxima are never NaN
 
 constexpr float kLog2e = 1.4426950408889634f;
