@@ -1,4 +1,6 @@
 """Attention over the NVFP4 KV cache at the ends of its number range."""
+import math
+
 import pytest
 import torch
 
@@ -59,3 +61,64 @@ def test_scores_far_below_zero(cuda_lib, dim, heads, group, new, kv):
         assert ref[1].max() < -5e34 and ((out.double() - ref[0]).abs() <= tol).all()
         # the factor is a product of five numbers, each rounded to 32 bits, and the change of base another
         assert ((lse.double() - ref[1]).abs() <= 2.0 ** -20 * ref[1].abs()).all()
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("heads,group,new,kv", SHAPES)
+def test_infinities(cuda_lib, dim, heads, group, new, kv):
+    """A query with an infinite element, and a head with an infinite decode
+    scale, have no softmax: NaNs, in that row and head and nowhere else.  With
+    keys of one sign every score of such a row is -inf, or every one +inf."""
+    t, table = _plain_keys(heads, new, kv, dim, seed=5)
+    rows, hq = sum(new), heads * group
+    q = torch.ones((rows, hq, dim), dtype=torch.bfloat16, device=DEV)
+    scale = dim ** -0.5
+    for at, x in ((5, -math.inf), (dim - 1, math.inf)):
+        for r, h in ((0, hq - 1), (rows - 1, 0)):
+            qx = q.clone()
+            qx[r, h, at] = x
+            hit = torch.zeros((rows, hq), dtype=torch.bool, device=DEV)
+            hit[r, h] = True
+            out, lse, _ = _call(qx, t, new, kv, table, scale)
+            ref = R.attention64(q, t, R.offsets(new), torch.tensor(kv), table, scale)
+            tol, tol_lse = R.attention_bounds(*ref, dim)
+            assert out[hit].isnan().all() and lse[hit].isnan().all()
+            assert ((out.double() - ref[0]).abs() <= tol)[~hit].all()
+            assert ((lse.double() - ref[1]).abs() <= tol_lse)[~hit].all()
+    for name in ("g_k", "g_v"):
+        for x in (-math.inf, math.inf):
+            g = t[name].clone()
+            g[heads - 1] = x
+            out, lse, _ = _call(q, {**t, name: g}, new, kv, table, scale)
+            assert out[:, -group:].isnan().all() and (name == "g_v" or lse[:, -group:].isnan().all())
+            assert not out[:, :-group].isnan().any() and not lse[:, :-group].isnan().any()
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("heads,group,new,kv", SHAPES)
+def test_scores_past_32_bits(cuda_lib, dim, heads, group, new, kv):
+    """Scores that are all -inf in 32 bits: NaNs, not the zeros of a row that sees nothing."""
+    t, table = _plain_keys(heads, new, kv, dim, seed=6)
+    q = torch.ones((sum(new), heads * group, dim), dtype=torch.bfloat16, device=DEV)
+    out, lse, _ = _call(q, t, new, kv, table, -1e37)
+    assert out.isnan().all() and lse.isnan().all()
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("new,kv", [([3, 4, 1], [2, 400, 500]), ([3, 4, 1], [2, 4000, 2000]), ([200, 90, 130], [150, 400, 700]),
+                                    ([100, 70, 90], [60, 5000, 90])])
+def test_infinities_in_rows_that_see_nothing(cuda_lib, dim, new, kv):
+    """Zeros and a log-sum of -inf where no position is visible: before position
+    0, or with a window whose pages are absent although others are there."""
+    heads, group, window = 2, 4, 20
+    t, table = _plain_keys(heads, new, kv, dim, seed=7)
+    table[1, 2:] = -1                                    # positions from 32 on: windows from 51 on see nothing
+    q = torch.full((sum(new), heads * group, dim), -math.inf, dtype=torch.bfloat16, device=DEV)
+    out, lse, _ = _call(q, t, new, kv, table, 0.1, window)
+    b = torch.repeat_interleave(torch.arange(3), torch.tensor(new))
+    i = torch.cat([torch.arange(n) for n in new])
+    pos = torch.tensor(kv)[b] - torch.tensor(new)[b] + i
+    sees = ((pos >= 0) & ((b != 1) | (pos - window + 1 < 32))).to(DEV)
+    assert 0 < int(sees.sum()) < len(pos)
+    assert out[sees].isnan().all() and lse[sees].isnan().all()
+    assert not out[~sees].any() and torch.isneginf(lse[~sees]).all()

@@ -110,4 +110,38 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLag = 8.0f;
 constexpr float kShift = 7.0f;
 
+// Whether a row at position pos of sequence b sees a key.  Asked where a row's
+// sum of weights is zero: its visible scores, if there are any, are then all
+// -inf (any finite one is a maximum at some point, and its weight not zero), and
+// such a row has no softmax.
+__device__ __forceinline__ bool sees_a_key(const AttnArgs& p, const SeqInfo& s, int b, int pos) {
+  const int end = min(pos, s.hi - 1);
+  for (int j = p.window > 0 ? max(pos - p.window + 1, 0) : 0; j <= end;) {
+    int at;
+    if (page_of(p.c, b, j, at) >= 0) return true;
+    j += p.c.page_size - at;
+  }
+  return false;
+}
+// The last b with off[b] <= row (row >= off[0], off ascending, n + 1 entries), by one thread.
+__device__ __forceinline__ int find_seq(const int32_t* __restrict__ off, int n, int row) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (__ldg(off + mid) <= row) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+// A row's sum of weights: zero for a row that sees nothing, NaN for one without
+// a softmax.
+__device__ __forceinline__ float row_sum(const AttnArgs& p, const SeqInfo& s, int b, int tok, float l) {
+  return l == 0.0f && sees_a_key(p, s, b, s.pos0 + tok) ? CUDART_NAN_F : l;
+}
+// What a row's sums are multiplied with.  Values are infinite or NaN (a code of
+// zero) where their decode scale is infinite: NaNs then, as for a NaN.
+__device__ __forceinline__ float row_factor(const AttnArgs& p, int head, float l) {
+  const float g = __ldg(p.c.g_v + head);
+  return l != 0.0f ? kScaleUnit * (g + (g - g)) / l : 0.0f;
+}
+
 }  // namespace quads

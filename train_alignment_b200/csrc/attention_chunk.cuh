@@ -403,7 +403,8 @@ __global__ void __launch_bounds__(kChThreads, 1) attention_chunk_kernel(AttnArgs
               }
             }
         } else {
-          const float inv = l != 0.0f ? kScaleUnit * __ldg(p.c.g_v + u.head) / l : 0.0f;
+          if (valid) l = row_sum(p, u.s, b, tok, l);
+          const float inv = row_factor(p, u.head, l);
           if (valid && p.lse != nullptr) p.lse[orow] = l != 0.0f ? -up * kLn2 + logf(l) : -CUDART_INF_F;
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
@@ -578,10 +579,12 @@ __global__ void __launch_bounds__(256) attention_join_kernel(AttnArgs p, int n_s
   const int64_t r = item / p.hq;
   const int h = static_cast<int>(item - r * p.hq);
   bool mine = false;
+  int b = -1;
+  SeqInfo s{};
   if (r < p.rows) {
-    const int b = warp_find_seq(p.off, p.c.n_seqs, static_cast<int>(r), lane);
+    b = warp_find_seq(p.off, p.c.n_seqs, static_cast<int>(r), lane);
     if (b >= 0) {
-      const SeqInfo s = seq_info(p, b);
+      s = seq_info(p, b);
       mine = r < s.r0 + s.nq;
     }
   }
@@ -621,7 +624,8 @@ __global__ void __launch_bounds__(256) attention_join_kernel(AttnArgs p, int n_s
   }
 #pragma unroll
   for (int k = 16; k; k >>= 1) l += __shfl_xor_sync(0xffffffffu, l, k);
-  const float inv = l != 0.0f ? kScaleUnit * __ldg(p.c.g_v + h / p.group) / l : 0.0f;
+  l = row_sum(p, s, b, static_cast<int>(r) - s.r0, l);
+  const float inv = row_factor(p, h / p.group, l);
   uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + at * D + lane * kE);
 #pragma unroll
   for (int e = 0; e < kE / 2; ++e) dst[e] = pack_bf16x2(o[2 * e] * inv, o[2 * e + 1] * inv);

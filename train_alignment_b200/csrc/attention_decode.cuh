@@ -599,11 +599,12 @@ __global__ void __launch_bounds__(kDecThreads, dec_ctas_per_sm(NT)) attention_de
         ll += ml_s[i][r].y * f;
       }
       if (whole) {
-        const float inv = ll != 0.0f ? kScaleUnit * __ldg(p.c.g_v + head) / ll : 0.0f;      // a NaN stays one
+        const int tok = static_cast<int>(fast_div(first_row + r, p.group_div));
+        ll = row_sum(p, s, b, tok, ll);
+        const float inv = row_factor(p, head, ll);
 #pragma unroll
         for (int i = 0; i < kDecWarps; ++i) f_s[i][r] *= inv;
         if (p.lse != nullptr) {
-          const int tok = static_cast<int>(fast_div(first_row + r, p.group_div));
           p.lse[static_cast<int64_t>(s.r0 + tok) * p.hq + head * p.group + (first_row + r - tok * p.group)] =
               ll != 0.0f ? (mm - kShift) * kLn2 + logf(ll) : -CUDART_INF_F;
         }
@@ -704,12 +705,17 @@ __global__ void __launch_bounds__(kJoinThreads * NT) attention_combine_kernel(At
     const int r = first_row + blockIdx.y + k * gridDim.y, tok = static_cast<int>(fast_div(r, p.group_div));
     return static_cast<int64_t>(r0 + tok) * p.hq + head * p.group + (r - tok * p.group);
   };
-  auto inverse = [&](float sum) { return sum != 0.0f ? kScaleUnit * __ldg(p.c.g_v + head) / sum : 0.0f; };
+  auto whole_sum = [&](int64_t row, float sum) {         // the sequence is looked for where it is needed
+    if (sum != 0.0f) return sum;
+    const int b = find_seq(p.off, p.c.n_seqs, r0);
+    return row_sum(p, seq_info(p, b), b, static_cast<int>(row / p.hq) - r0, sum);
+  };
   auto log_sum = [&](float max, float sum) { return sum != 0.0f ? (max - kShift) * kLn2 + logf(sum) : -CUDART_INF_F; };
   if (alone) {
     if (mine < rows) {
       const int64_t row = row_of(mine);
-      const float inv = inverse(l);
+      l = whole_sum(row, l);
+      const float inv = row_factor(p, head, l);
       reinterpret_cast<uint2*>(p.out + row * D)[lane] = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
       if (lane == 0 && p.lse != nullptr) p.lse[row] = log_sum(m, l);
     }
@@ -730,7 +736,8 @@ __global__ void __launch_bounds__(kJoinThreads * NT) attention_combine_kernel(At
       o += reinterpret_cast<const float*>(o_s[g])[d] * f;
     }
     const int64_t row = row_of(k);
-    p.out[row * D + d] = static_cast<uint16_t>(float_to_bf16_bits(o * inverse(l)));
+    l = whole_sum(row, l);
+    p.out[row * D + d] = static_cast<uint16_t>(float_to_bf16_bits(o * row_factor(p, head, l)));
     if (d == 0 && p.lse != nullptr) p.lse[row] = log_sum(m, l);
   }
 }
