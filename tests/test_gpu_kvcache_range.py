@@ -122,3 +122,21 @@ def test_infinities_in_rows_that_see_nothing(cuda_lib, dim, new, kv):
     assert 0 < int(sees.sum()) < len(pos)
     assert out[sees].isnan().all() and lse[sees].isnan().all()
     assert not out[~sees].any() and torch.isneginf(lse[~sees]).all()
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("ratio", [2.0 ** 10, 2.0 ** 18, 2.0 ** 24])
+@pytest.mark.parametrize("heads,group,new,kv", SHAPES[:7])
+def test_a_query_of_wide_spread(cuda_lib, dim, ratio, heads, group, new, kv):
+    """One element `ratio` times the others, where every key is zero: the scores
+    are those of the others, to 32 bits."""
+    n_pages = sum(-(-n // 16) for n in kv) + 2
+    t = R.make_cache(n_pages, heads, 16, dim, 8, DEV)
+    t["k_codes"][..., 3] &= 0x0F                         # element 7
+    table = R.make_table(kv, 16, n_pages, max(-(-n // 16) for n in kv), 9)
+    g = torch.Generator().manual_seed(10)
+    q = torch.randn((sum(new), heads * group, dim), generator=g).to(torch.bfloat16).to(DEV)
+    q[..., 7] = ratio
+    out, lse, ref = _call(q, t, new, kv, table, dim ** -0.5)
+    tol, tol_lse = R.attention_bounds(*ref, dim)
+    assert ((out.double() - ref[0]).abs() <= tol).all() and ((lse.double() - ref[1]).abs() <= tol_lse).all()

@@ -57,15 +57,18 @@ __device__ __forceinline__ SeqInfo seq_info(const AttnArgs& p, int b) {
 }
 
 // Queries are multiplied as 16-bit floats with 11 significant bits: a row is
-// scaled by a power of two that brings its largest element to [1, 2), which
-// keeps every BF16 element down to 2^-17 of the largest exact (smaller ones
-// are off by 2^-25 of the largest).  Returns the row's exponent field.
+// scaled by a power of two that brings its largest element to [2^14, 2^15), which
+// keeps every BF16 element down to 2^-31 of the largest exact (smaller ones
+// are off by 2^-39 of the largest).  The largest FP16 of a BF16 element is
+// then 2^16 - 2^8 and a product of D with cached values at most 2^27, far from
+// FP32's range.  Returns the row's exponent field, within what both factors hold.
+constexpr uint32_t kQueryExp = 14;
 __device__ __forceinline__ uint32_t row_exponent(uint32_t max_bf16_bits) {
   const uint32_t e = (max_bf16_bits >> 7) & 0xFFu;
-  return min(max(e, 1u), 253u);
+  return min(max(e, kQueryExp + 1u), 253u);
 }
-__device__ __forceinline__ float exp_field_up(uint32_t e) { return __uint_as_float(e << 23); }              // 2^(e - 127)
-__device__ __forceinline__ float exp_field_down(uint32_t e) { return __uint_as_float((254u - e) << 23); }   // 2^(127 - e)
+__device__ __forceinline__ float exp_field_up(uint32_t e) { return __uint_as_float((e - kQueryExp) << 23); }           // 2^(e - 127 - 14)
+__device__ __forceinline__ float exp_field_down(uint32_t e) { return __uint_as_float((254u + kQueryExp - e) << 23); }  // 2^(127 + 14 - e)
 
 // Two BF16 (a word) times r -> two FP16.
 __device__ __forceinline__ uint32_t bf16x2_scaled_f16x2(uint32_t w, float r) {
