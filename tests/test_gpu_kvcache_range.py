@@ -140,3 +140,17 @@ def test_a_query_of_wide_spread(cuda_lib, dim, ratio, heads, group, new, kv):
     out, lse, ref = _call(q, t, new, kv, table, dim ** -0.5)
     tol, tol_lse = R.attention_bounds(*ref, dim)
     assert ((out.double() - ref[0]).abs() <= tol).all() and ((lse.double() - ref[1]).abs() <= tol_lse).all()
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_read_without_a_page_beside_a_scale_that_is_not_a_number(cuda_lib, dim):
+    """Zeros where there is no page, whatever the head's decode scale."""
+    t = R.make_cache(4, 2, 16, dim, 11, DEV)
+    t["g_k"][1] = math.nan
+    t["g_v"][0] = math.inf
+    off = torch.tensor([0, 40], dtype=torch.int32, device=DEV)
+    table = torch.tensor([[2, -1, 1]], dtype=torch.int32, device=DEV)
+    for dt in (B.OUT_F32, B.OUT_BF16):
+        k, v = B.kv_cache_read(_cache(t), off, table, 40, out_dtype=dt)
+        assert not k[16:32].any() and not v[16:32].any()
+        assert k[:16, 1].isnan().all() and k[32:, 0].any() and not k[:, 0].isnan().any() and not v[:, 1].isnan().any()

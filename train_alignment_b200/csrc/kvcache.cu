@@ -193,9 +193,11 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(CacheArgs c, void* __
       const int i = i0 + u * kThreads;
       if (i >= total) break;
       const Block x = block_of(map, i);
-      if (page_s[x.r] == -2) continue;
+      const int page = page_s[x.r];
+      if (page == -2) continue;
       const bool is_v = one_side || x.second;
-      const float g = __ldg((is_v ? c.g_v : c.g_k) + x.head), sv = e4m3_value(s[u]);
+      const float gh = __ldg((is_v ? c.g_v : c.g_k) + x.head), sv = e4m3_value(s[u]);
+      const float g = page < 0 ? 0.0f : gh;            // a scale that is NaN or infinite would make a zero code NaN
       const uint64_t sv2 = pack_f32x2(sv, sv), g2 = pack_f32x2(g, g);
       uint32_t h[2][4];
       e2m1x8_to_f16x2(codes[u].x, h[0]);
