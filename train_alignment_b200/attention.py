@@ -17,7 +17,10 @@ from . import workloads as W
 class KVCache:
     """A paged NVFP4 key/value cache: codes [n_pages, n_heads, page_size, D / 2],
     scales [n_pages, n_heads, page_size, D / 16], decode scales g [n_heads].
-    Wraps the given tensors; KVCache.empty allocates them."""
+    Wraps the given tensors; KVCache.empty allocates them.  The calls go by the
+    tensors' addresses, so the attributes cannot be set: other tensors are
+    another KVCache (values are changed in place, storage is not; a deep copy has
+    its own)."""
 
     def __init__(self, k_codes, k_scales, v_codes, v_scales, g_k, g_v):
         codes, dev = k_codes.shape, k_codes.get_device()
@@ -38,11 +41,21 @@ class KVCache:
                 ("g_k", g_k), ("g_v", g_v)))
             raise ValueError(f"a cache needs contiguous uint8 codes {tuple(codes)}, uint8 scales {scales} and float32 "
                              f"decode scales {heads} on one device, got {got}")
-        self.n_pages, self.n_heads, self.page_size, self.head_dim = n_pages, n_heads, page_size, 2 * half
-        self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
-        self.g_k, self.g_v = g_k, g_v
-        self.desc = B.kv_cache_desc(n_pages, page_size, n_heads, 2 * half, 0, k_codes.data_ptr(), k_scales.data_ptr(),
+        a = self.__dict__
+        a["n_pages"], a["n_heads"], a["page_size"], a["head_dim"] = n_pages, n_heads, page_size, 2 * half
+        a["k_codes"], a["k_scales"], a["v_codes"], a["v_scales"] = k_codes, k_scales, v_codes, v_scales
+        a["g_k"], a["g_v"] = g_k, g_v
+        a["desc"] = B.kv_cache_desc(n_pages, page_size, n_heads, 2 * half, 0, k_codes.data_ptr(), k_scales.data_ptr(),
                                     v_codes.data_ptr(), v_scales.data_ptr(), g_k.data_ptr(), g_v.data_ptr())
+
+    def __setattr__(self, name, value):
+        raise AttributeError(f"a KVCache's {name} cannot be changed: make another KVCache")
+
+    def __delattr__(self, name):
+        raise AttributeError(f"a KVCache's {name} cannot be changed: make another KVCache")
+
+    def __reduce__(self):                                # copies describe their own tensors
+        return type(self), (self.k_codes, self.k_scales, self.v_codes, self.v_scales, self.g_k, self.g_v)
 
     @classmethod
     def empty(cls, n_pages, page_size, n_heads, head_dim, amax_k, amax_v, device="cuda"):
