@@ -7,6 +7,7 @@ import pytest
 import torch
 
 from train_alignment_b200 import attention as A
+from train_alignment_b200 import binding as B
 
 TENSORS = ("k_codes", "k_scales", "v_codes", "v_scales", "g_k", "g_v")
 
@@ -46,3 +47,29 @@ def test_copies_describe_their_own_tensors():
         assert _addresses(x) == _own(x) and x.page_size == 16 and x.head_dim == 64
         for n in TENSORS:
             assert torch.equal(getattr(x, n), getattr(c, n))
+
+
+def test_gradients_are_not_cut_in_silence():
+    """Arguments that require a gradient are refused while autograd records, and
+    pass on to the other checks (here: host tensors) where it does not."""
+    c = A.KVCache.empty(3, 32, 2, 64, 6.0, 6.0, device="cpu")
+    x = torch.zeros((4, 2, 64), dtype=torch.bfloat16)
+    y = x.clone().requires_grad_()
+    i = torch.zeros(2, dtype=torch.int32)
+    pos, freq = torch.zeros(4, dtype=torch.int64), torch.zeros(32, dtype=torch.float64)
+    learned = freq.clone().requires_grad_()
+    calls = [lambda: B.kv_cache_write(c, y, x, i, i[:1], i.view(1, 2)), lambda: B.kv_cache_write(c, x, y * 2, i, i[:1], i.view(1, 2)),
+             lambda: B.attention_paged(y, c, i, i[:1], i.view(1, 2), 4), lambda: B.rope(y, None, pos, freq),
+             lambda: B.rope(x, y, pos, freq), lambda: B.rope(x, None, pos, learned),
+             lambda: B.rope_backward(x, y, pos, freq)]
+    for call in calls:
+        with pytest.raises(ValueError, match="requires a gradient"):
+            call()
+        with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):
+            call()
+        with torch.inference_mode(), pytest.raises(ValueError, match="CUDA"):
+            call()
+    parts = [getattr(c, n) for n in TENSORS]
+    for at in (4, 5):
+        with pytest.raises(ValueError, match="detached"):
+            A.KVCache(*[p.clone().requires_grad_() if j == at else p for j, p in enumerate(parts)])

@@ -41,6 +41,8 @@ class KVCache:
                 ("g_k", g_k), ("g_v", g_v)))
             raise ValueError(f"a cache needs contiguous uint8 codes {tuple(codes)}, uint8 scales {scales} and float32 "
                              f"decode scales {heads} on one device, got {got}")
+        if g_k.requires_grad or g_v.requires_grad:
+            raise ValueError("a cache's decode scales are fixed while its tokens are in use: pass detached tensors")
         a = self.__dict__
         a["n_pages"], a["n_heads"], a["page_size"], a["head_dim"] = n_pages, n_heads, page_size, 2 * half
         a["k_codes"], a["k_scales"], a["v_codes"], a["v_scales"] = k_codes, k_scales, v_codes, v_scales

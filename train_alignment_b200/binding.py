@@ -708,6 +708,16 @@ def _stream(t, name):
     return torch._C._cuda_getCurrentRawStream(d)
 
 
+def _refuse_gradients(call, instead):
+    """For tensors that require a gradient: these calls take no part in autograd,
+    and would hand back results without one in silence."""
+    if torch.is_grad_enabled():
+        raise ValueError(f"{call}: an argument requires a gradient, which this call does not pass on; {instead}")
+
+
+_DETACH = "pass detached tensors, or call it under torch.no_grad()"
+
+
 def _like(t, first, dtype, shape, name):
     """t's pointer, after checking that it is a contiguous tensor of that type
     and shape on the device of `first`."""
@@ -744,7 +754,10 @@ def _tables(cache, row_off, block_table):
 
 
 def kv_cache_write(cache, k, v, row_off, kv_len, block_table):
-    """Quantize k, v [rows, n_heads, D] into the cache's pages (quads_kv_cache_write)."""
+    """Quantize k, v [rows, n_heads, D] into the cache's pages (quads_kv_cache_write).
+    No gradients: k or v that requires one is refused while autograd records."""
+    if k.requires_grad or v.requires_grad:
+        _refuse_gradients("kv_cache_write", _DETACH)
     stream = _stream(cache.k_codes, "the cache")
     rows, heads, dim, ld_k = _heads_view(k, cache.k_codes, "k")
     rows_v, heads_v, dim_v, ld_v = _heads_view(v, cache.k_codes, "v")
@@ -786,6 +799,8 @@ def kv_cache_read(cache, row_off, block_table, rows, start=None, out_dtype=OUT_B
 
 
 def _rope(q, k, positions, freq, interleaved, mscale, inverse, q_out, k_out):
+    if q.requires_grad or freq.requires_grad or (k is not None and k.requires_grad):
+        _refuse_gradients("rope_backward" if inverse else "rope", _DETACH + " (rope_backward gives rope's gradients)")
     stream = _stream(q, "q")
     rows, hq, dim, ld_q = _heads_view(q, q, "q")
     hk = ld_k = ld_ko = 0
@@ -818,7 +833,9 @@ def _rope(q, k, positions, freq, interleaved, mscale, inverse, q_out, k_out):
 def rope(q, k, positions, freq, interleaved=False, mscale=1.0, q_out=None, k_out=None):
     """Rotary positions of q [rows, heads, D] and k (may be None); freq [rot_dim
     / 2] float64 radians per position, positions [rows] int64.  Returns
-    (q_out, k_out); the outputs may be the inputs."""
+    (q_out, k_out); the outputs may be the inputs.  Its gradients are
+    rope_backward's: arguments that require one are refused while autograd
+    records."""
     return _rope(q, k, positions, freq, interleaved, mscale, False, q_out, k_out)
 
 
@@ -835,7 +852,10 @@ def attention_paged(q, cache, row_off, kv_len, block_table, max_q_len, scale=Non
                     ws=None):
     """Attention of the new tokens' q [rows, heads_q, D] over the paged cache
     (quads_attention_paged): out [rows, heads_q, D]; lse [rows, heads_q] is
-    filled when given.  scale None: D ** -0.5."""
+    filled when given.  scale None: D ** -0.5.  No gradients: q that requires
+    one is refused while autograd records."""
+    if q.requires_grad:
+        _refuse_gradients("attention_paged", _DETACH)
     first = cache.k_codes
     stream = _stream(first, "the cache")
     rows, hq, dim, ld_q = _heads_view(q, first, "q")
