@@ -77,6 +77,8 @@ int quads_device_status(quads_stream_t stream);
  * wait gives up, records a timeout and the kernel returns.  A following
  * quads_device_status() returns QUADS_ERR_TIMEOUT. */
 int quads_selftest_bounded_wait(uint64_t timeout_ns, quads_stream_t stream);
+/* The same of the attention's waits, which record their timeouts apart. */
+int quads_selftest_attention_wait(uint64_t timeout_ns, quads_stream_t stream);
 /* Output tile of the grouped FP4 GEMMs with the BF16 correction (or none)
  * and N % 256 == 0 (a tuning and testing switch, not a reading of the pages):
  *   0  128 x 128 on one CTA, the correction in its own FP32 accumulator;

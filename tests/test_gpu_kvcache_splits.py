@@ -1,4 +1,5 @@
-"""Chunks whose keys are split many ways, and the cache's calls in a CUDA graph."""
+"""Chunks whose keys are split many ways, the cache's calls in a CUDA graph, and
+the attention's bounded waits."""
 import pytest
 import torch
 
@@ -71,3 +72,14 @@ def test_rotate_write_and_read_in_a_graph(cuda_lib, dim, inter):
         for n in ("k_codes", "k_scales", "v_codes", "v_scales"):
             assert torch.equal(getattr(cache, n), getattr(other, n))
     assert B.device_status() == B.OK
+
+
+def test_a_wait_that_runs_out_is_reported_once(cuda_lib):
+    """Each of the two records of timeouts is read and cleared, and a call works after."""
+    tests = (B.selftest_attention_wait, B.selftest_bounded_wait)
+    for calls in (tests[:1], tests[1:], tests):
+        assert B.device_status() == B.OK
+        for f in calls:
+            f(2_000_000)                               # 2 ms on a barrier that nothing completes
+        assert B.device_status() == B.ERR_TIMEOUT and B.device_status() == B.OK
+    _attend(2, 4, 64, 16, [100], [300], seed=61)

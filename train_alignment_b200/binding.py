@@ -68,6 +68,7 @@ _SIGS = {
     "quads_launch_count": (c_u64, []),
     "quads_device_status": (c_i32, [c_vp]),
     "quads_selftest_bounded_wait": (c_i32, [c_u64, c_vp]),
+    "quads_selftest_attention_wait": (c_i32, [c_u64, c_vp]),
     "quads_gemm_set_tile_shape": (c_i32, [c_i32]),
     "quads_gemm_set_decode_rows": (c_i32, [c_i32]),
     "quads_set_sm_budget": (c_i32, [c_i32]),
@@ -204,6 +205,10 @@ def device_status():
 
 def selftest_bounded_wait(timeout_ns):
     _check(load().quads_selftest_bounded_wait(int(timeout_ns), _s()), "quads_selftest_bounded_wait")
+
+
+def selftest_attention_wait(timeout_ns):
+    _check(load().quads_selftest_attention_wait(int(timeout_ns), _s()), "quads_selftest_attention_wait")
 
 
 TILE_128x128, TILE_128x256, TILE_PAIR_256x256 = 0, 1, 2

@@ -21,6 +21,19 @@ int attention_wait_status(unsigned int* v) {
 
 namespace {
 
+// One thread waits on a barrier that nothing completes, as the kernel for many
+// rows waits; the wait gives up after limit_ns and records the timeout.
+__global__ void attention_wait_selftest_kernel(uint64_t limit_ns) {
+  __shared__ __align__(8) uint64_t bar;
+  __shared__ int abort_flag;
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    mbar_init(smem_addr(&bar), 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    ch_wait(smem_addr(&bar), 0, &abort_flag, limit_ns);
+  }
+}
+
 // Launches a kernel that may become resident before the one in front of it in
 // the stream has ended, and waits for that itself.
 template <typename... Params, typename... Args>
@@ -173,6 +186,14 @@ int launch_chunk(AttnArgs p, const ChunkPlan& plan, void* ws, cudaStream_t strea
 using namespace quads;
 
 extern "C" {
+
+int quads_selftest_attention_wait(uint64_t timeout_ns, quads_stream_t stream) {
+  clear_error();
+  QUADS_REQUIRE(timeout_ns > 0 && timeout_ns <= 10000000000ull, QUADS_ERR_INVALID_ARG, "timeout must be in (0, 10 s]");
+  attention_wait_selftest_kernel<<<1, 32, 0, stream>>>(timeout_ns);
+  count_launches(1);
+  return check_launch("attention_wait_selftest_kernel");
+}
 
 size_t quads_attention_paged_workspace_bytes(const quads_kv_cache* cache, int64_t rows, int heads_q, int n_seqs,
                                              int max_pages, int max_q_len) {
