@@ -78,8 +78,11 @@ constexpr int kDecMaxParts = 192;
 // have but a tile or two.
 constexpr int kDecUnitCost = 3;
 
-size_t dec_workspace(int D, int nt) {
-  return static_cast<size_t>(dec_grid(nt)) * (2 * (8 * nt) * (D * sizeof(float) + sizeof(float2)) + sizeof(int4));
+// The parts of units that runs share, and where a run can be long enough, what
+// its warps take out of their accumulators.
+size_t dec_workspace(int D, int nt, bool keep) {
+  const size_t kept = keep ? kDecWarps * dec_kept_floats(D, nt) * sizeof(float) : 0;
+  return static_cast<size_t>(dec_grid(nt)) * (2 * (8 * nt) * (D * sizeof(float) + sizeof(float2)) + sizeof(int4) + kept);
 }
 
 // Keys that a unit can see, at most.
@@ -94,24 +97,37 @@ int64_t dec_keys(const quads_kv_cache* c, int max_pages, int max_q_len, int wind
 // more than that.
 constexpr int kDecWhole = 8;
 bool dec_whole(int64_t keys) { return keys <= kDecWhole * kDecTile; }
+int dec_min_quota(int64_t tiles) { return static_cast<int>(ceil_div(tiles, int64_t(kDecMaxParts))); }
+int64_t dec_units(const quads_kv_cache* c, int n_seqs, int64_t unit_rows, int nt) {
+  return static_cast<int64_t>(n_seqs) * c->n_heads * ceil_div(unit_rows, int64_t(8) * nt);
+}
+// Whether a warp can have so many steps in a unit that its sums are begun anew.
+bool dec_keeps(int64_t units, int64_t tiles, int nt) {
+  const int64_t run = ceil_div(units * (tiles + kDecUnitCost), int64_t(dec_grid(nt))), least = dec_min_quota(tiles);
+  return tiles > kDecKeep && (run > least ? run : least) >= kDecKeep;
+}
 
 template <int D, int NT>
-int launch_decode(AttnArgs p, void* ws, int unit_rows, int64_t keys, bool whole, cudaStream_t stream) {
+int launch_decode(AttnArgs p, const quads_kv_cache* cache, void* ws, int unit_rows, int64_t keys, bool whole, cudaStream_t stream) {
   const int grid = dec_grid(NT);
   p.row_groups = (unit_rows + 8 * NT - 1) / (8 * NT);
-  const int64_t units = static_cast<int64_t>(p.c.n_seqs) * p.c.n_heads * p.row_groups;
+  const int64_t units = dec_units(cache, p.c.n_seqs, unit_rows, NT);
   const int64_t tiles = ceil_div(keys, int64_t(kDecTile));
   if (whole) {
-    attention_decode_kernel<D, NT, true><<<static_cast<unsigned>(units < grid ? units : grid), kDecThreads, 0, stream>>>(p, 0);
+    attention_decode_kernel<D, NT, true, false><<<static_cast<unsigned>(units < grid ? units : grid), kDecThreads, 0, stream>>>(p, 0);
     count_launches(1);
     return check_launch("attention_decode_kernel");
   }
   p.cuts = static_cast<int4*>(ws);
   p.part_o = reinterpret_cast<float*>(p.cuts + grid);
   p.part_ml = reinterpret_cast<float2*>(p.part_o + static_cast<size_t>(2) * grid * (8 * NT) * D);
+  if (dec_keeps(units, tiles, NT)) p.kept = reinterpret_cast<float*>(p.part_ml + static_cast<size_t>(2) * grid * (8 * NT));
   p.by_unit = units <= grid;
   p.unit_cost = units * tiles >= 2 * grid ? kDecUnitCost : 0;
-  attention_decode_kernel<D, NT, false><<<grid, kDecThreads, 0, stream>>>(p, static_cast<int>(ceil_div(tiles, int64_t(kDecMaxParts))));
+  if (p.kept != nullptr)
+    attention_decode_kernel<D, NT, false, true><<<grid, kDecThreads, 0, stream>>>(p, dec_min_quota(tiles));
+  else
+    attention_decode_kernel<D, NT, false, false><<<grid, kDecThreads, 0, stream>>>(p, dec_min_quota(tiles));
   QUADS_TRY(check_launch("attention_decode_kernel"));
   // the join: rows on blocks of their own as far as there are SMs for them
   const int64_t x = p.by_unit ? units : grid, per = num_sms() / x;
@@ -127,14 +143,16 @@ int launch_decode(AttnArgs p, void* ws, int unit_rows, int64_t keys, bool whole,
 struct ChunkPlan {
   int64_t blocks;
   int n_split;
+  bool keep;           // contexts can be so long that sums are begun anew
 };
 ChunkPlan chunk_plan(const quads_kv_cache* c, int64_t rows, int heads_q, int n_seqs, int max_pages, int max_q_len) {
   const int64_t group = heads_q / c->n_heads;
   const int64_t by_rows = rows * group / kChRows + n_seqs;
   const int64_t by_seqs = ceil_div(static_cast<int64_t>(max_q_len) * group, int64_t(kChRows)) * n_seqs;
-  ChunkPlan p{by_rows < by_seqs ? by_rows : by_seqs, 1};
+  ChunkPlan p{by_rows < by_seqs ? by_rows : by_seqs, 1, false};
   const int64_t units = p.blocks * c->n_heads;
   const int64_t tiles = ceil_div(static_cast<int64_t>(max_pages) * c->page_size, int64_t(kChTile));
+  p.keep = tiles > kChKeep;
   int64_t n = units > 0 ? num_sms() / units : 1;
   if (n > tiles / kChMinTiles) n = tiles / kChMinTiles;
   // no more than 256 MB of parts (a call with many rows of no sequence)
@@ -144,32 +162,33 @@ ChunkPlan chunk_plan(const quads_kv_cache* c, int64_t rows, int heads_q, int n_s
   return p;
 }
 
-size_t chunk_workspace(const quads_kv_cache* c, int64_t rows, int heads_q, int n_split) {
-  if (n_split <= 1) return 0;
-  return static_cast<size_t>(n_split) * rows * heads_q * (c->head_dim * sizeof(float) + sizeof(float2));
+size_t chunk_workspace(const quads_kv_cache* c, int64_t rows, int heads_q, const ChunkPlan& p) {
+  if (p.n_split <= 1 && !p.keep) return 0;
+  return static_cast<size_t>(p.n_split) * rows * heads_q * (c->head_dim * sizeof(float) + sizeof(float2));
 }
 
 // The softmax warpgroups wait for registers that the others give up, which adds
 // up only if the kernel was compiled to 128 a thread.
-template <int D>
+template <int D, bool kKeep>
 bool chunk_registers_add_up() {
   static const bool ok = [] {
     cudaFuncAttributes a{};
-    return cudaFuncGetAttributes(&a, attention_chunk_kernel<D>) == cudaSuccess && a.numRegs == kChRegs;
+    return cudaFuncGetAttributes(&a, attention_chunk_kernel<D, kKeep>) == cudaSuccess && a.numRegs == kChRegs;
   }();
   return ok;
 }
 
-template <int D>
+template <int D, bool kKeep>
 int launch_chunk(AttnArgs p, const ChunkPlan& plan, void* ws, cudaStream_t stream) {
   p.part_o = static_cast<float*>(ws);
   p.part_ml = reinterpret_cast<float2*>(p.part_o + static_cast<size_t>(plan.n_split) * p.rows * p.hq * D);
-  QUADS_REQUIRE(chunk_registers_add_up<D>(), QUADS_ERR_CUDA, "attention_chunk_kernel is not compiled to %d registers", kChRegs);
+  p.kept = p.part_o;
+  QUADS_REQUIRE((chunk_registers_add_up<D, kKeep>()), QUADS_ERR_CUDA, "attention_chunk_kernel is not compiled to %d registers", kChRegs);
   const int smem = ch_smem_bytes(D);
-  if (cudaFuncSetAttribute(attention_chunk_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+  if (cudaFuncSetAttribute(attention_chunk_kernel<D, kKeep>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
     return check_launch("attention_chunk_kernel attributes");
   const dim3 grid(static_cast<unsigned>(plan.blocks * p.c.n_heads), plan.n_split);
-  attention_chunk_kernel<D><<<grid, kChThreads, smem, stream>>>(p, plan.n_split);
+  attention_chunk_kernel<D, kKeep><<<grid, kChThreads, smem, stream>>>(p, plan.n_split);
   count_launches(1);
   QUADS_TRY(check_launch("attention_chunk_kernel"));
   if (plan.n_split > 1) {
@@ -202,9 +221,10 @@ size_t quads_attention_paged_workspace_bytes(const quads_kv_cache* cache, int64_
   const int64_t unit_rows = static_cast<int64_t>(max_q_len) * (heads_q / cache->n_heads);
   if (few_rows(cache, n_seqs, unit_rows)) {               // without a window, with which a call may need none
     const int64_t keys = dec_keys(cache, max_pages, max_q_len, 0);
-    return dec_whole(keys) ? 0 : dec_workspace(cache->head_dim, unit_rows <= 8 ? 1 : 2);
+    const int nt = unit_rows <= 8 ? 1 : 2;
+    return dec_whole(keys) ? 0 : dec_workspace(cache->head_dim, nt, dec_keeps(dec_units(cache, n_seqs, unit_rows, nt), ceil_div(keys, int64_t(kDecTile)), nt));
   }
-  return chunk_workspace(cache, rows, heads_q, chunk_plan(cache, rows, heads_q, n_seqs, max_pages, max_q_len).n_split);
+  return chunk_workspace(cache, rows, heads_q, chunk_plan(cache, rows, heads_q, n_seqs, max_pages, max_q_len));
 }
 
 int quads_attention_paged(const uint16_t* q, int64_t rows, int64_t ld_q, int heads_q, const quads_kv_cache* cache,
@@ -249,13 +269,15 @@ int quads_attention_paged(const uint16_t* q, int64_t rows, int64_t ld_q, int hea
     const int64_t keys = dec_keys(cache, max_pages, max_q_len, window);
     const bool whole = dec_whole(keys);
     if (cache->head_dim == 64)
-      return n <= 8 ? launch_decode<64, 1>(p, ws, n, keys, whole, stream) : launch_decode<64, 2>(p, ws, n, keys, whole, stream);
-    return n <= 8 ? launch_decode<128, 1>(p, ws, n, keys, whole, stream) : launch_decode<128, 2>(p, ws, n, keys, whole, stream);
+      return n <= 8 ? launch_decode<64, 1>(p, cache, ws, n, keys, whole, stream) : launch_decode<64, 2>(p, cache, ws, n, keys, whole, stream);
+    return n <= 8 ? launch_decode<128, 1>(p, cache, ws, n, keys, whole, stream) : launch_decode<128, 2>(p, cache, ws, n, keys, whole, stream);
   }
   const ChunkPlan plan = chunk_plan(cache, rows, heads_q, n_seqs, max_pages, max_q_len);
   QUADS_REQUIRE(plan.blocks * cache->n_heads < (int64_t(1) << 31) && ceil_div(rows * heads_q, int64_t(8)) < (int64_t(1) << 31),
                 QUADS_ERR_UNSUPPORTED_SHAPE, "too many rows");
-  return cache->head_dim == 64 ? launch_chunk<64>(p, plan, ws, stream) : launch_chunk<128>(p, plan, ws, stream);
+  if (plan.keep)
+    return cache->head_dim == 64 ? launch_chunk<64, true>(p, plan, ws, stream) : launch_chunk<128, true>(p, plan, ws, stream);
+  return cache->head_dim == 64 ? launch_chunk<64, false>(p, plan, ws, stream) : launch_chunk<128, false>(p, plan, ws, stream);
 }
 
 }  // extern "C"

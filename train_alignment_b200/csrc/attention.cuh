@@ -22,6 +22,9 @@ struct AttnArgs {
   // unnormalised sums, and {maximum, sum} of each row
   float* part_o;
   float2* part_ml;
+  // sums taken out of the matrix instructions' accumulators (few rows: by CTA
+  // and warp; many: in part_o), or null where no sum is long enough for that
+  float* kept;
   // {slot of the first part or -1, CTA of the last, the sequence's first row *
   // n_heads + head, rows | first of them << 8} of each unit (by_unit), or of
   // the one that each CTA begins and does not end
@@ -30,6 +33,13 @@ struct AttnArgs {
   int row_groups;           // units of a sequence and key head, at most
   int unit_cost;            // what beginning and ending a unit costs, in key tiles
 };
+
+// A matrix instruction adds the products of 16 keys to its FP32 sum and
+// truncates: a sum of n additions comes out about n 2^-24 too small (measured
+// with values of one sign: 2^16 additions 0.6 %, more than the rounding to
+// BF16).  So after this many it is added to another in memory, rounded, and
+// begun anew: 2^-11.4 at most.
+constexpr int kMaxAdds = 4096;
 
 // A sequence of a call: its rows, and the keys that they can see.
 struct SeqInfo {

@@ -171,6 +171,8 @@ __device__ __forceinline__ uint32_t move_trans(uint32_t x) {
 // key i of a matrix of eight is row i ^ (i / 2 % 2) of the group: both matrix
 // operands are then read without bank conflicts.
 constexpr int kDecStages = 2;
+constexpr int kDecKeep = kMaxAdds / kDecSub;          // steps after which a warp's sums are begun anew
+__host__ __device__ constexpr int dec_kept_floats(int D, int nt) { return 32 * (2 * nt + D / 4 * nt); }     // of a warp
 __host__ __device__ constexpr int dec_stage_bytes(int D) { return 16 * (D + D / 8); }
 __device__ __forceinline__ int dec_key(int i) { return i ^ ((i >> 1) & 1); }
 
@@ -253,7 +255,9 @@ struct DecRaw {
   }
 };
 
-template <int D, int NT, bool kWhole>
+// kWhole: a CTA takes whole units.  kKeep: a run can have more than kDecKeep
+// steps of a unit (an instance of its own: in the other it cost 1 %).
+template <int D, int NT, bool kWhole, bool kKeep>
 __global__ void __launch_bounds__(kDecThreads, dec_ctas_per_sm(NT)) attention_decode_kernel(AttnArgs p, int min_quota) {
   constexpr int kRows = 8 * NT;
   constexpr int kMT = D / 16;                           // 16-element tiles of O^T
@@ -529,9 +533,32 @@ __global__ void __launch_bounds__(kDecThreads, dec_ctas_per_sm(NT)) attention_de
       }
     };
 
+    // the sums of kDecKeep steps to those before, in memory (each lane its own):
+    // rescaled from the maxima that they were kept at
+    float* const kept = p.kept + (static_cast<size_t>(blockIdx.x) * kDecWarps + warp) * dec_kept_floats(D, NT) + lane;
+    auto keep = [&](bool first, bool back) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float* const at = kept + 32 * (2 * n + i);
+          const float f = first ? 0.0f : ex2(up[n][i] - *at);
+          *at = up[n][i];
+#pragma unroll
+          for (int d = 0; d < kMT; ++d)
+#pragma unroll
+            for (int k = i; k < 4; k += 2) {
+              float* const x = kept + 32 * (2 * NT + (n * kMT + d) * 4 + k);
+              const float sum = first ? o[n][d][k] : __fmaf_rn(*x, f, o[n][d][k]);
+              if (!back) *x = sum;
+              o[n][d][k] = back ? sum : 0.0f;
+            }
+        }
+    };
     uint32_t gone_cur = gone_now;
     constexpr int kTurn = 32 / kDecSub;                 // steps of a look-up
     for (int step0 = 0; step0 < steps; step0 += kDecStages) {
+      if (kKeep && step0 > 0 && step0 % kDecKeep == 0) keep(step0 == kDecKeep, false);
 #pragma unroll
       for (int u = 0; u < kDecStages; ++u) {             // step0 + u lies in place u of the ring
         const int step = step0 + u;
@@ -556,6 +583,7 @@ __global__ void __launch_bounds__(kDecThreads, dec_ctas_per_sm(NT)) attention_de
         attend(ring + u * kStage, j_first + step * kDecTile, (gone_cur >> (kDecSub * (step % kTurn))) & ((1u << kDecSub) - 1u));
       }
     }
+    if (kKeep && steps > kDecKeep) keep(false, true);
     cp_async_wait<0>();
     __syncthreads();
 
