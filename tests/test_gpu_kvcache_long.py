@@ -105,3 +105,14 @@ def test_long_sums_whose_maximum_grows(cuda_lib, dim, heads, group, length, new)
         ref = (full * total[0] + w * v[1, :, :last].sum(1)) / den
         _check(out[r].double(), lse[r].double(), ref.repeat_interleave(group, 0),
                torch.full((heads * group,), scale * dim + math.log(den), dtype=torch.float64, device=DEV))
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("new", [1, 90])
+@pytest.mark.parametrize("window", [(1 << 30) - 12345, (1 << 30) + (1 << 28) + 77])
+def test_windows_around_2_to_the_30(cuda_lib, dim, new, window):
+    """Windows past 2^30 are as long as they say."""
+    kv = (1 << 30) + (1 << 29) - 54321
+    # the places of a part of a page are seen once more than the others: too little to be seen here, so
+    # the log-sum tells the windows apart: 2^-14 of 2^30 positions are 2^16
+    _check(*_long(1, 1, dim, [kv], [new], window=window))

@@ -258,7 +258,7 @@ int quads_attention_paged(const uint16_t* q, int64_t rows, int64_t ld_q, int hea
   p.c = cache_args(cache, block_table, n_seqs, max_pages);
   p.q = q; p.out = out; p.lse = lse; p.off = row_off; p.kv_len = kv_len;
   p.rows = rows; p.ld_q = ld_q; p.hq = heads_q; p.group = heads_q / cache->n_heads;
-  p.max_q = max_q_len; p.window = window < (1 << 30) ? window : (1 << 30); p.scale = scale;
+  p.max_q = max_q_len; p.window = window; p.scale = scale;
   p.group_div = make_fastdiv(static_cast<uint32_t>(p.group));
   const int64_t unit_rows = static_cast<int64_t>(max_q_len) * p.group;
   if (few_rows(cache, n_seqs, unit_rows)) {

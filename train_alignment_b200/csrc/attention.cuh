@@ -49,6 +49,12 @@ struct SeqInfo {
   int lo, hi;  // keys [lo, hi), lo a multiple of 16
 };
 
+// The first position that a row at pos sees: of a window, or 0.  (Rows before
+// position 0 see none; pos - window stays within 32 bits for the others.)
+__device__ __forceinline__ int first_seen(const AttnArgs& p, int pos) {
+  return p.window > 0 ? max(max(pos, -1) - p.window + 1, 0) : 0;
+}
+
 __device__ __forceinline__ SeqInfo seq_info(const AttnArgs& p, int b) {
   const int rows = static_cast<int>(p.rows);
   const int r0 = min(max(__ldg(p.off + b), 0), rows), r1 = min(max(__ldg(p.off + b + 1), r0), rows);
@@ -129,7 +135,7 @@ constexpr float kShift = 7.0f;
 // such a row has no softmax.
 __device__ __forceinline__ bool sees_a_key(const AttnArgs& p, const SeqInfo& s, int b, int pos) {
   const int end = min(pos, s.hi - 1);
-  for (int j = p.window > 0 ? max(pos - p.window + 1, 0) : 0; j <= end;) {
+  for (int j = first_seen(p, pos); j <= end;) {
     int at;
     if (page_of(p.c, b, j, at) >= 0) return true;
     j += p.c.page_size - at;

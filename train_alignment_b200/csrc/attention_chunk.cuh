@@ -146,7 +146,7 @@ __device__ __forceinline__ void ch_range(const AttnArgs& p, const SeqInfo& s, in
   const int pos_a = s.pos0 + static_cast<int>(fast_div(row0, p.group_div));
   const int pos_b = s.pos0 + static_cast<int>(fast_div(last, p.group_div));
   const int hi = max(min(s.hi, pos_b + 1), s.lo);
-  const int lo = min(max(p.window > 0 ? pos_a - p.window + 1 : 0, s.lo), hi);
+  const int lo = min(max(first_seen(p, pos_a), s.lo), hi);
   a = (lo - s.lo) / kChTile;
   b = (hi - s.lo + kChTile - 1) / kChTile;
 }
@@ -297,7 +297,7 @@ __global__ void __launch_bounds__(kChThreads, 1) attention_chunk_kernel(AttnArgs
 
       const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
       const uint32_t s_col = tmem + lane_base, p_col = s_col + kChPCol + 64 * i, o_col = s_col + kChOCol + kChTile * i;
-      const int pos = u.s.pos0 + tok;
+      const int pos = u.s.pos0 + tok, from = first_seen(p, pos);
       float up = kShift - kNoMax, l = 0.0f;
       bool ok = true;
       // the row's place among the parts: there too are the sums that were taken out of O_i, at a maximum of up
@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(kChThreads, 1) attention_chunk_kernel(AttnArgs
         const int j0 = u.s.lo + t * kChTile;
         // columns [first, last] of the tile are seen
         const int last = valid ? min(pos, u.s.hi - 1) - j0 : -1;
-        const int first = p.window > 0 ? pos - p.window + 1 - j0 : 0;
+        const int first = from - j0;
         uint32_t gone = gone_s[(t - u.t0) & 7];        // two bits in each byte: eight groups of 16 keys
         gone = (gone & 3u) | ((gone >> 6) & 0xCu) | ((gone >> 12) & 0x30u) | ((gone >> 18) & 0xC0u);
         const bool masked = __any_sync(0xffffffffu, last < kChTile - 1 || first > 0 || gone != 0);

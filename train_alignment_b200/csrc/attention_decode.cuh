@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(kDecThreads, dec_ctas_per_sm(NT)) attention_de
     // keys share a page: lane i looks up the cache row of group i of 32, the
     // next 32 half way through these.  A group without a page reads row 0 and
     // masks it.
-    const int pos_last = s.pos0 + s.nq - 1;
+    const int from_last = first_seen(p, s.pos0 + s.nq - 1);             // the last row's first key
     const int j_first = s.lo + tile0 * kDecTile + 16 * kDecSub * warp;
     const int steps = min(tile1 - tile0, (s.hi - j_first + kDecTile - 1) / kDecTile);     // those with a key below hi
     auto lookup = [&](int group) -> uint32_t {
@@ -443,7 +443,7 @@ __global__ void __launch_bounds__(kDecThreads, dec_ctas_per_sm(NT)) attention_de
 #pragma unroll
           for (int i = 0; i < 4; ++i) y[h][n][i] = __fmaf_rn(sc[h][n][i], c2[n][i & 1], up[n][i & 1]);
       constexpr int kKeys = 16 * kDecSub;
-      if (gone || j0 + kKeys - 1 > s.pos0 || j0 + kKeys > s.hi || (p.window > 0 && j0 <= pos_last - p.window)) {
+      if (gone || j0 + kKeys - 1 > s.pos0 || j0 + kKeys > s.hi || j0 < from_last) {
 #pragma unroll
         for (int h = 0; h < kDecSub; ++h)
 #pragma unroll
@@ -452,7 +452,7 @@ __global__ void __launch_bounds__(kDecThreads, dec_ctas_per_sm(NT)) attention_de
             for (int i = 0; i < 4; ++i) {
               const int j = j0 + 16 * h + dec_key(g) + 8 * (i >> 1);
               const int pos = s.pos0 + static_cast<int>(fast_div(first_row + 8 * n + 2 * t + (i & 1), p.group_div));
-              const bool see = !((gone >> h) & 1u) && j <= pos && j < s.hi && (p.window <= 0 || j > pos - p.window);
+              const bool see = !((gone >> h) & 1u) && j <= pos && j < s.hi && j >= first_seen(p, pos);
               if (!see) y[h][n][i] = -CUDART_INF_F;
             }
       }
