@@ -668,7 +668,7 @@ int quads_rope(const uint16_t* q, int64_t ld_q, int heads_q, const uint16_t* k, 
  * position) and, when window > 0, j > p - window; k and v are the cached
  * values of head h / (heads_q / n_heads).  A row with no such j gets zeros;
  * otherwise a NaN or an infinity in q[r][h] or in the head's decode scales
- * gives NaNs, and so do scores that are all -inf in 32 bits.
+ * gives NaNs, and scores past FP32's range may.
  *   q, out    BF16 [rows][heads_q][D], q's rows ld_q elements apart
  *             (a multiple of 8), out's contiguous; 16-byte aligned.  heads_q
  *             is a multiple of n_heads.  out must not overlap q.

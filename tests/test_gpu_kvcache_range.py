@@ -154,3 +154,56 @@ def test_read_without_a_page_beside_a_scale_that_is_not_a_number(cuda_lib, dim):
         k, v = B.kv_cache_read(_cache(t), off, table, 40, out_dtype=dt)
         assert not k[16:32].any() and not v[16:32].any()
         assert k[:16, 1].isnan().all() and k[32:, 0].any() and not k[:, 0].isnan().any() and not v[:, 1].isnan().any()
+
+
+def _range(q, t, new, kv, table, scale):
+    """Per row and head: the least and greatest of each element among the values
+    of the keys whose 64-bit scores are within 2 d of the largest, d = dim 2^-23
+    + 2^-22 of the largest sum of |terms| (what scores in 32 bits can be off
+    by), and 40 more (the others weigh less than 2^-57 each); the largest score;
+    d."""
+    k, v = R.values64(t, "k"), R.values64(t, "v")
+    (rows, hq, dim), heads, page = q.shape, k.shape[1], k.shape[2]
+    lo, hi = torch.empty((2, rows, hq, dim), dtype=torch.float64, device=DEV)
+    top, far = torch.empty((2, rows, hq), dtype=torch.float64, device=DEV)
+    r0 = 0
+    for b, (n, length) in enumerate(zip(new, kv)):
+        j = torch.arange(length)
+        at, place = table[b, j // page].long().to(DEV), (j % page).to(DEV)
+        see = j.to(DEV)[None] <= torch.arange(length - n, length, device=DEV)[:, None]
+        for h in range(hq):
+            kk, vv = k[at, h * heads // hq, place], v[at, h * heads // hq, place]
+            x = q[r0:r0 + n, h].double()
+            s = (x @ kk.T * scale).masked_fill(~see, -math.inf)
+            m = s.amax(1, keepdim=True)
+            d = (x.abs() @ kk.abs().T * abs(scale)).masked_fill(~see, 0.0).amax(1, keepdim=True) * (dim * 2.0 ** -23 + 2.0 ** -22)
+            for i in range(n):
+                near = vv[(s[i] >= m[i] - 2 * d[i] - 40)]
+                lo[r0 + i, h], hi[r0 + i, h] = near.amin(0), near.amax(0)
+            top[r0:r0 + n, h], far[r0:r0 + n, h] = m[:, 0], d[:, 0]
+        r0 += n
+    return lo, hi, top, far
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("size", [1e4, 1e6, 1e8, 1e10, 1e20, 1e30])
+@pytest.mark.parametrize("heads,group,new,kv", SHAPES)
+def test_huge_scores(cuda_lib, dim, size, heads, group, new, kv):
+    """Finite scores of any size and both signs: a row is a mean of the values of
+    the keys that scores in 32 bits cannot tell from the first, mostly one."""
+    n_pages = sum(-(-n // 16) for n in kv) + 2
+    t = R.make_cache(n_pages, heads, 16, dim, 12, DEV)
+    table = R.make_table(kv, 16, n_pages, max(-(-n // 16) for n in kv), 13)
+    g = torch.Generator().manual_seed(14)
+    q = torch.randn((sum(new), heads * group, dim), generator=g).to(torch.bfloat16).to(DEV)
+    for scale in (size, -size):
+        off, lens = R.offsets(new).to(DEV), torch.tensor(kv, dtype=torch.int32, device=DEV)
+        lse = torch.empty(q.shape[:2], device=DEV)
+        out = B.attention_paged(q, _cache(t), off, lens, table.to(DEV), max(new), scale=scale, lse=lse).double()
+        assert B.device_status() == B.OK and not out.isnan().any() and not lse.isnan().any()
+        lo, hi, top, d = _range(q, t, new, kv, table, scale)
+        # a weight and a sum rounded as in attention_bounds, of values at most the range's largest; rounding to BF16
+        tol = (2.0 ** -8 + 2.0 ** -10) * torch.maximum(lo.abs(), hi.abs()) + 2.0 ** -30
+        assert ((out >= lo - tol) & (out <= hi + tol)).all()
+        assert (lo == hi).all(-1).float().mean() > 0.9
+        assert ((lse.double() - top).abs() <= d + math.log(max(kv)) + 2.0 ** -20 * top.abs()).all()

@@ -124,10 +124,25 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 // A row's running maximum may fall this far (in powers of two) behind a new
 // score before its sums are rescaled; weights are kept at 2^kShift times
-// their value so that FP16 holds them from 2^-31 (2^-21 as a normal number)
-// to 2^15 of the maximum's.
+// their value so that FP16 holds them from 2^-31 of the maximum's (2^-21 as a
+// normal number) to 2^8.
 constexpr float kLag = 8.0f;
 constexpr float kShift = 7.0f;
+// A weight is 2^(c (x - top) + kShift), x the matrix instructions' product, top
+// the row's largest so far, c its factor.  c is positive; not zero, so that a
+// first product is always above kNoMax and -inf times it is no NaN.
+constexpr float kLeastFactor = 1e-37f;
+// The kernel for many rows has it as one FMA, c x + shift.  The shift is
+// rounded, alike for a row's weights, which does not matter up to kFar; at 2^27
+// it is by more than what FP16 holds.
+constexpr float kFar = 16384.0f;
+__device__ __forceinline__ float row_shift(float top, float c) { return top > kNoMax ? __fmaf_rn(-top, c, kShift) : -kNoMax; }
+__device__ __forceinline__ bool is_far(float shift) { return fabsf(shift) > kFar && fabsf(shift) < -kNoMax; }
+// What sums shrink by when the largest product grows.  (0 times an infinite c is
+// NaN, which fminf drops.)
+__device__ __forceinline__ float row_shrink(float top, float now, float c) { return ex2(fminf((top - now) * c, 0.0f)); }
+// A row's largest score (to powers of two), as the joins compare it.
+__device__ __forceinline__ float row_max(float top, float c) { return top > kNoMax ? top * c : kNoMax; }
 
 // Whether a row at position pos of sequence b sees a key.  Asked where a row's
 // sum of weights is zero: its visible scores, if there are any, are then all

@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(kChThreads, 1) attention_chunk_kernel(AttnArgs
         // does a NaN, which would reach masked scores too
         c2 = p.scale * kLog2e * kScaleUnit * __ldg(p.c.g_k + u.head) * exp_field_up(e);
         const float sign = c2 < 0.0f ? -down : c2 == c2 ? down : c2;
-        c2 = fmaxf(fabsf(c2), 1e-37f);                  // not zero, which times -inf were NaN
+        c2 = fmaxf(fabsf(c2), kLeastFactor);
         const uint32_t dst = q_s + i * kTB + r * 128;
 #pragma unroll
         for (int j = 0; j < D / 8; ++j)
@@ -298,9 +298,9 @@ __global__ void __launch_bounds__(kChThreads, 1) attention_chunk_kernel(AttnArgs
       const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
       const uint32_t s_col = tmem + lane_base, p_col = s_col + kChPCol + 64 * i, o_col = s_col + kChOCol + kChTile * i;
       const int pos = u.s.pos0 + tok, from = first_seen(p, pos);
-      float up = kShift - kNoMax, l = 0.0f;
-      bool ok = true;
-      // the row's place among the parts: there too are the sums that were taken out of O_i, at a maximum of up
+      float xm = kNoMax, up = -kNoMax, l = 0.0f;        // the largest product so far; what is added to scores
+      bool ok = true, far = false;
+      // the row's place among the parts: there too are the sums that were taken out of O_i, at a largest of xm
       const auto part_at = [&] { return (static_cast<int64_t>(blockIdx.y) * p.rows + u.s.r0 + tok) * p.hq + head_q; };
       for (int t = ta[i]; t < tb[i]; ++t) {
         ok = ch_wait_warp(s_full(i), (t - ta[i]) & 1, abort_flag);
@@ -342,12 +342,23 @@ __global__ void __launch_bounds__(kChThreads, 1) attention_chunk_kernel(AttnArgs
           for (int e = 0; e < 4; ++e) mx[e] = fmax3(mx[e], x[k + e], x[k + 4 + e]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], x[124 + e]);
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c2;
-        if (__any_sync(0xffffffffu, top + up > kShift + kLag)) {
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        if (far || __any_sync(0xffffffffu, (top - xm) * c2 > kLag)) {
           // a new maximum: the first tile's, or one that has grown by kLag
-          const float un = fminf(up, kShift - top);
-          const float a = ex2(un - up);
-          up = un;
+          const float xn = fmaxf(xm, top), a = row_shrink(xm, xn, c2);
+          xm = xn;
+          up = row_shift(xn, c2);
+          far = __any_sync(0xffffffffu, is_far(up));
+          if (far && is_far(up)) {                      // every tile then comes here
+            const uint64_t xm2 = pack_f32x2(-xm, -xm);
+#pragma unroll
+            for (int k = 0; k < kChTile; k += 2) {
+              const uint64_t z = fadd2(pack_f32x2(x[k], x[k + 1]), xm2);
+              x[k] = lo_f32(z);
+              x[k + 1] = hi_f32(z);
+            }
+            up = kShift;
+          }
           l *= a;
           if (t > ta[i]) {
             ok = ch_wait_warp(pv_done(i), (t - 1 - ta[i]) & 1, abort_flag);
@@ -388,8 +399,8 @@ __global__ void __launch_bounds__(kChThreads, 1) attention_chunk_kernel(AttnArgs
         if (kKeep && t > ta[i] && ((t - ta[i]) & (kChKeep - 1)) == 0) {   // the next product begins O_i anew
           const int64_t at = part_at();
           const bool first = t - ta[i] == kChKeep;
-          const float f = first || !valid ? 0.0f : ex2(up - p.part_ml[at].x);
-          if (valid) p.part_ml[at].x = up;
+          const float f = first || !valid ? 0.0f : row_shrink(p.part_ml[at].x, xm, c2);
+          if (valid) p.part_ml[at].x = xm;
 #pragma unroll 1
           for (int c = 0; c < D / 16; ++c) {
             uint32_t o[16];
@@ -414,14 +425,14 @@ __global__ void __launch_bounds__(kChThreads, 1) attention_chunk_kernel(AttnArgs
         const bool some = tb[i] > ta[i];
         const int64_t orow = static_cast<int64_t>(u.s.r0 + tok) * p.hq + head_q, at = part_at();
         const bool kept = kKeep && valid && tb[i] - ta[i] > kChKeep;
-        const float f = kept ? ex2(up - p.part_ml[at].x) : 0.0f;
+        const float f = kept ? row_shrink(p.part_ml[at].x, xm, c2) : 0.0f;
         const auto add_kept = [&](uint32_t (&x)[32], int c) {
           const float* const src = p.kept + at * D + 32 * c;
 #pragma unroll
           for (int k = 0; k < 32; ++k) x[k] = __float_as_uint(__fmaf_rn(src[k], f, __uint_as_float(x[k])));
         };
         if (n_split > 1) {
-          if (valid) p.part_ml[at] = make_float2(kShift - up, l);
+          if (valid) p.part_ml[at] = make_float2(row_max(xm, c2), l);
           if (some)
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
@@ -438,7 +449,7 @@ __global__ void __launch_bounds__(kChThreads, 1) attention_chunk_kernel(AttnArgs
         } else {
           if (valid) l = row_sum(p, u.s, b, tok, l);
           const float inv = row_factor(p, u.head, l);
-          if (valid && p.lse != nullptr) p.lse[orow] = l != 0.0f ? -up * kLn2 + logf(l) : -CUDART_INF_F;
+          if (valid && p.lse != nullptr) p.lse[orow] = l != 0.0f ? (row_max(xm, c2) - kShift) * kLn2 + logf(l) : -CUDART_INF_F;
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             uint32_t x[32];

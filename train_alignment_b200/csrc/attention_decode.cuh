@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(kDecThreads, dec_ctas_per_sm(NT)) attention_de
     uint32_t qf[NT][D / 8];
     float c2[NT][2];                                    // score factor (to powers of two) of rows 2t, 2t + 1
     {
-      const float base_f = p.scale * kLog2e * kScaleUnit * __ldg(p.c.g_k + head);
+      const float base_f = p.scale * kLog2e * kScaleUnit * __ldg(p.c.g_k + head);      // its sign, or that it is NaN, goes to the queries
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const int r = 8 * n + g;
@@ -384,22 +384,21 @@ __global__ void __launch_bounds__(kDecThreads, dec_ctas_per_sm(NT)) attention_de
         mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
         const uint32_t e = row_exponent(mx);
-        const float down = exp_field_down(e);
+        const float down = base_f < 0.0f ? -exp_field_down(e) : base_f == base_f ? exp_field_down(e) : base_f;
 #pragma unroll
         for (int i = 0; i < D / 8; ++i) qf[n][i] = bf16x2_scaled_f16x2(qf[n][i], down);
-        const float f = base_f * exp_field_up(e);       // row g's factor; rows 2t, 2t + 1 are lanes 8t, 8t + 4
+        const float f = fmaxf(fabsf(base_f) * exp_field_up(e), kLeastFactor);       // row g's factor; rows 2t, 2t + 1 are lanes 8t, 8t + 4
         c2[n][0] = __shfl_sync(0xffffffffu, f, 8 * t);
         c2[n][1] = __shfl_sync(0xffffffffu, f, 8 * t + 4);
       }
     }
-    // up: kShift minus a row's running maximum, so that one FMA gives the
-    // exponent of a weight
-    float o[NT][kMT][4], up[NT][2], l[NT][2];
+    // xm: a row's largest product so far
+    float o[NT][kMT][4], xm[NT][2], l[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
       for (int i = 0; i < kMT; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.0f;
-      up[n][0] = up[n][1] = kShift - kNoMax;
+      xm[n][0] = xm[n][1] = kNoMax;
       l[n][0] = l[n][1] = 0.0f;
     }
 
@@ -441,7 +440,7 @@ __global__ void __launch_bounds__(kDecThreads, dec_ctas_per_sm(NT)) attention_de
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) y[h][n][i] = __fmaf_rn(sc[h][n][i], c2[n][i & 1], up[n][i & 1]);
+          for (int i = 0; i < 4; ++i) y[h][n][i] = __fmaf_rn(sc[h][n][i] - xm[n][i & 1], c2[n][i & 1], kShift);
       constexpr int kKeys = 16 * kDecSub;
       if (gone || j0 + kKeys - 1 > s.pos0 || j0 + kKeys > s.hi || j0 < from_last) {
 #pragma unroll
@@ -474,13 +473,12 @@ __global__ void __launch_bounds__(kDecThreads, dec_ctas_per_sm(NT)) attention_de
             for (int h = 0; h < kDecSub; ++h)
 #pragma unroll
               for (int k = i; k < 4; k += 2)
-                if (y[h][n][k] > -CUDART_INF_F) z = fmaxf(z, sc[h][n][k] * c2[n][i]);
+                if (y[h][n][k] > -CUDART_INF_F) z = fmaxf(z, sc[h][n][k]);
             z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, 4));
             z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, 8));
             z = fmaxf(z, __shfl_xor_sync(0xffffffffu, z, 16));
-            const float un = fminf(up[n][i], kShift - z);
-            const float a = ex2(un - up[n][i]);
-            up[n][i] = un;
+            const float xn = fmaxf(xm[n][i], z), a = row_shrink(xm[n][i], xn, c2[n][i]);
+            xm[n][i] = xn;
             l[n][i] *= a;
 #pragma unroll
             for (int d = 0; d < kMT; ++d) {
@@ -491,7 +489,7 @@ __global__ void __launch_bounds__(kDecThreads, dec_ctas_per_sm(NT)) attention_de
             for (int h = 0; h < kDecSub; ++h)
 #pragma unroll
               for (int k = i; k < 4; k += 2)
-                if (y[h][n][k] > -CUDART_INF_F) y[h][n][k] = __fmaf_rn(sc[h][n][k], c2[n][i], un);
+                if (y[h][n][k] > -CUDART_INF_F) y[h][n][k] = __fmaf_rn(sc[h][n][k] - xn, c2[n][i], kShift);
           }
       }
       uint32_t pb[kDecSub][NT][2];
@@ -542,8 +540,8 @@ __global__ void __launch_bounds__(kDecThreads, dec_ctas_per_sm(NT)) attention_de
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           float* const at = kept + 32 * (2 * n + i);
-          const float f = first ? 0.0f : ex2(up[n][i] - *at);
-          *at = up[n][i];
+          const float f = first ? 0.0f : row_shrink(*at, xm[n][i], c2[n][i]);
+          *at = xm[n][i];
 #pragma unroll
           for (int d = 0; d < kMT; ++d)
 #pragma unroll
@@ -597,7 +595,7 @@ __global__ void __launch_bounds__(kDecThreads, dec_ctas_per_sm(NT)) attention_de
         x += __shfl_xor_sync(0xffffffffu, x, 8);
         x += __shfl_xor_sync(0xffffffffu, x, 16);
         const int r = 8 * n + 2 * t + i;
-        if (g == 0) ml_s[warp][r] = make_float2(kShift - up[n][i], x);
+        if (g == 0) ml_s[warp][r] = make_float2(row_max(xm[n][i], c2[n][i]), x);
         float4* dst = reinterpret_cast<float4*>(&o_s[warp][r][g * (D / 8)]);
 #pragma unroll
         for (int d = 0; d < kMT / 2; ++d)
