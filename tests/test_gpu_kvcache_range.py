@@ -207,3 +207,22 @@ def test_huge_scores(cuda_lib, dim, size, heads, group, new, kv):
         assert ((out >= lo - tol) & (out <= hi + tol)).all()
         assert (lo == hi).all(-1).float().mean() > 0.9
         assert ((lse.double() - top).abs() <= d + math.log(max(kv)) + 2.0 ** -20 * top.abs()).all()
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("new,kv,rows", [([3, 6], [40, 50], 5), ([3, 6], [2000, 1500], 5), ([90, 120], [300, 400], 150),
+                                         ([100], [6000], 70), ([5], [3], 4)])
+def test_fewer_rows_than_the_offsets_name(cuda_lib, dim, new, kv, rows):
+    """Rows have the positions that the offsets give them, also where the call
+    ends before the last sequence does."""
+    t = R.make_cache(800, 2, 16, dim, 15, DEV)
+    table = R.make_table(kv, 16, 800, max(-(-n // 16) for n in kv), 16)
+    off, lens = R.offsets(new).to(DEV), torch.tensor(kv, dtype=torch.int32, device=DEV)
+    q = torch.randn((sum(new), 8, dim), generator=torch.Generator().manual_seed(17)).to(torch.bfloat16).to(DEV)
+    ref = R.attention64(q, t, off, lens, table, 0.1)
+    tol, tol_lse = (x[:rows] for x in R.attention_bounds(*ref, dim))
+    lse = torch.empty((rows, 8), device=DEV)
+    out = B.attention_paged(q[:rows], _cache(t), off, lens, table.to(DEV), max(new), scale=0.1, lse=lse)
+    empty = torch.isneginf(ref[1][:rows])
+    assert ((out.double() - ref[0][:rows]).abs() <= tol).all() and torch.equal(torch.isneginf(lse), empty)
+    assert ((lse.double() - ref[1][:rows])[~empty].abs() <= tol_lse[~empty]).all()

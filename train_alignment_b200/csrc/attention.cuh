@@ -57,12 +57,13 @@ __device__ __forceinline__ int first_seen(const AttnArgs& p, int pos) {
 
 __device__ __forceinline__ SeqInfo seq_info(const AttnArgs& p, int b) {
   const int rows = static_cast<int>(p.rows);
-  const int r0 = min(max(__ldg(p.off + b), 0), rows), r1 = min(max(__ldg(p.off + b + 1), r0), rows);
+  const int off0 = __ldg(p.off + b), off1 = __ldg(p.off + b + 1);
+  const int r0 = min(max(off0, 0), rows), r1 = min(max(off1, r0), rows);
   SeqInfo s;
   s.r0 = r0;
-  const int n = r1 - r0;
-  s.nq = min(n, p.max_q);
-  const int64_t pos0 = static_cast<int64_t>(max(__ldg(p.kv_len + b), 0)) - n;      // > -2^30: rows < 2^30
+  s.nq = min(r1 - r0, p.max_q);
+  // rows are fewer than 2^30: all are before position 0 if the first is that far
+  const int64_t pos0 = max(static_cast<int64_t>(max(__ldg(p.kv_len + b), 0)) - (static_cast<int64_t>(off1) - off0), -(int64_t(1) << 30));
   s.pos0 = static_cast<int>(pos0);
   const int64_t cap = p.c.n_pages > 0 ? static_cast<int64_t>(p.c.max_pages) * p.c.page_size : 0;
   s.hi = static_cast<int>(max(int64_t(0), min(cap, pos0 + s.nq)));
