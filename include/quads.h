@@ -672,16 +672,22 @@ int quads_rope(const uint16_t* q, int64_t ld_q, int heads_q, const uint16_t* k, 
  *   q, out    BF16 [rows][heads_q][D], q's rows ld_q elements apart
  *             (a multiple of 8), out's contiguous; 16-byte aligned.  heads_q
  *             is a multiple of n_heads.  out must not overlap q.
- *   max_q_len at least the rows of the longest sequence (a longer sequence's
- *             rows past it are not computed); the work is laid out by it.
+ *   max_q_len at least the rows of the longest sequence; the work is laid out
+ *             by it.  Rows past it, and those of no sequence, are untouched.
  *   max_pages at most (2^31 - 2^16) / page_size.
  *   lse       (nullable) device float [rows][heads_q]: log sum_j exp(scale
  *             q . k_j), -inf for a row of zeros.
  *   ws        device workspace of quads_attention_paged_workspace_bytes()
  *             bytes, 16-byte aligned; calls that can run at the same time
  *             need their own.
- * Scores, softmax statistics and sums are FP32.  A device wait that exceeds
- * ~4 s records a timeout (quads_device_status). */
+ * Scores, softmax statistics and sums are FP32.  Rounded to fewer bits besides
+ * the result: a query element below 2^-31 of its row's largest (by 2^-39 of
+ * that), and each weight to FP16 before it multiplies a value (by 2^-11 of it;
+ * by 2^-32 of the row's largest where it is below 2^-21 of that).  A sum of
+ * values may come out up to 2^-11 too small (the matrix instructions truncate).
+ * The workspace is larger where max_pages * page_size passes 65536: a call
+ * with many rows then needs rows * heads_q * (4 D + 8) bytes at least.
+ * A device wait that exceeds ~4 s records a timeout (quads_device_status). */
 size_t quads_attention_paged_workspace_bytes(const quads_kv_cache* cache, int64_t rows, int heads_q, int n_seqs,
                                              int max_pages, int max_q_len);
 int quads_attention_paged(const uint16_t* q, int64_t rows, int64_t ld_q, int heads_q, const quads_kv_cache* cache,

@@ -777,7 +777,9 @@ def kv_cache_write(cache, k, v, row_off, kv_len, block_table):
 
 def kv_cache_read(cache, row_off, block_table, rows, start=None, out_dtype=OUT_BF16, k_out=None, v_out=None):
     """Cached keys and values [rows, n_heads, D] of each sequence from position
-    start[b] (0) on (quads_kv_cache_read); given outputs are written in place."""
+    start[b] (0) on (quads_kv_cache_read); given outputs are written in place.
+    Rows of no sequence are left as they are: without outputs they hold whatever
+    the memory did."""
     first = cache.k_codes
     stream = _stream(first, "the cache")
     n, m, off, table = _tables(cache, row_off, block_table)
@@ -857,8 +859,10 @@ def attention_paged(q, cache, row_off, kv_len, block_table, max_q_len, scale=Non
                     ws=None):
     """Attention of the new tokens' q [rows, heads_q, D] over the paged cache
     (quads_attention_paged): out [rows, heads_q, D]; lse [rows, heads_q] is
-    filled when given.  scale None: D ** -0.5.  No gradients: q that requires
-    one is refused while autograd records."""
+    filled when given.  scale None: D ** -0.5.  Rows that are not computed (of no
+    sequence, past max_q_len) are left as they are: without `out` they hold
+    whatever the memory did, so a padded batch passes a filled one.  No
+    gradients: q that requires one is refused while autograd records."""
     if q.requires_grad:
         _refuse_gradients("attention_paged", _DETACH)
     first = cache.k_codes

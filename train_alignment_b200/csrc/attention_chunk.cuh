@@ -1,5 +1,6 @@
-// Attention of many rows (chunks of prompts, groups of more than 16 rows):
-// bound by the tensor cores and by the exponentials.
+// Attention of many rows of a sequence and key head (chunks of prompts: more
+// than 48, or than 64 where the sequences' key heads are few): bound by the
+// tensor cores and by the exponentials.
 //
 // A CTA takes 256 rows (two tiles of 128) of one key head: row r of a
 // sequence is query head r % group of its token r / group, so the rows share
@@ -25,8 +26,8 @@
 // Measured on chunks of 4096 and 3793 tokens that end contexts of 12000 and
 // 9909, 32 query and 8 key heads of 128 (1.17 TFLOP): 0.87 ms alone, 1340
 // TFLOP/s, 0.82 of the measured burst of a library product; back to back under
-// the power cap 0.96 ms, 0.89 of its sustained rate.  The tensor pipe is active
-// 65 % of the cycles and so is the unit of exponentials; leaving out the
+// the power cap 0.97 ms in a graph, 0.87 of its sustained rate (1.00 ms as
+// called with changing inputs, 0.85).  The tensor pipe is active 64 % of the cycles and so is the unit of exponentials; leaving out the
 // exponentials changes nothing, leaving out the conversion 12 %.  The products'
 // issue was the limit before: from one lane in a divergent branch 1.31 ms.
 //

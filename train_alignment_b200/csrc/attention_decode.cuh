@@ -24,17 +24,17 @@
 // exact in FP16.
 //
 // Why these instructions and not tcgen05 as in the kernel for many rows: of
-// about 280 instructions for 16 keys, 128 convert codes and apply scales, which
+// about 285 instructions for 16 keys, 128 convert codes and apply scales, which
 // every layout needs; with keys in tensor memory the stores and the softmax on
 // 128 lanes come to about 240, while a tile of 128 rows for 4 queries would
 // wait on its own products.  Two groups of 16 keys at once hide each other's
 // latency (one group, and four CTAs an SM instead of three: an eighth slower).
 //
-// Four contexts of up to 65536, 32 / 8 heads of 128 (170 MB): 38.4 us, 4.4 TB/s.
+// Four contexts of up to 65536, 32 / 8 heads of 128 (170 MB): 38.4 us in a graph, 4.4 TB/s (41.0 as called).
 // Of an earlier 43.9 the copies alone took 38.9, and conversion and scaling
 // could hide but 2.8: what bounds it is the memory and a run's two ends.  Its
 // first keys land 3.8 us after the launch, the join takes 2.5 (64 contexts of
-// up to 4096, 87 MB: 25.1 us).  A deeper ring, the next unit's copies under this
+// up to 4096, 87 MB: 25.1 us; 28.7 as called).  A deeper ring, the next unit's copies under this
 // one's join, the values' products a step behind the scores' and unequal runs
 // for the CTAs that share an SM changed nothing or cost 2 to 7 %.
 #pragma once
